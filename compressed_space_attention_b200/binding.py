@@ -69,6 +69,18 @@ SIGNATURES = [
     ("isoq_decode_static_workspace_bytes", _SZ, []),
     ("isoq_decode_attention_static", _I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I64, _I, _I,
                                           _I, _P, _P, _F, _P, _P]),
+    ("isoq_decode_window_workspace_size", _SZ, [_I, _I, _I, _I64, _I, _I64, _I64]),
+    ("isoq_decode_attention_window", _I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I64, _I, _I, _I, _P, _P, _F,
+                                          _I64, _I64, _P, _P, _SZ, _P]),
+    ("isoq_prefill_attention_window", _I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _I, _I, _I, _P, _P,
+                                           _F, _I64, _I64, _P, _P]),
+    ("isoq_decode_prefix_workspace_size", _SZ, [_I, _I, _I, _I64, _I64, _I]),
+    ("isoq_decode_attention_prefix", _I, [_P, _I, _P, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I, _I, _I,
+                                          _I64, _I, _I, _I, _P, _P, _F, _P, _P, _SZ, _P]),
+    ("isoq_build_block_tables", _I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _P]),
+    ("isoq_paged_append", _I, [_P, _P, _I, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
+    ("isoq_paged_decode_attention", _I, [_P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I64, _I, _I, _I,
+                                         _P, _P, _F, _I64, _I64, _P, _P, _SZ, _P]),
 ]
 
 _lib = None
@@ -491,3 +503,280 @@ def isoq_decode_attention_static(q, packed_k, packed_v, norms_k, norms_v, seq_le
 
 def isoq_decode_static_workspace_bytes() -> int:
     return lib().isoq_decode_static_workspace_bytes()
+
+
+# ---------------------------------------------------------------------------
+# Serving attention: window and sinks, shared prefix, pages
+# ---------------------------------------------------------------------------
+
+def _scale(scale: Optional[float], d: int) -> float:
+    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+
+def _contiguous(**tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _typed(dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _check_cache(packed_k, packed_v, norms_k, norms_v, d, bits):
+    """Shapes and types of a packed cache [a][b][c][d*bits/8] with its norms
+    [a][b][c]; returns its shape."""
+    torch = _torch()
+    _typed(torch.uint8, packed_k=packed_k, packed_v=packed_v)
+    _typed(torch.float16, norms_k=norms_k, norms_v=norms_v)
+    if packed_k.shape != packed_v.shape or packed_k.shape[:-1] != norms_k.shape or norms_k.shape != norms_v.shape:
+        raise ValueError("packed K, packed V and their norms do not have one shape")
+    if packed_k.shape[-1] != isoq_packed_bytes(d, bits):
+        raise ValueError("packed row size does not match d and bits")
+    return packed_k.shape
+
+
+def _check_params(params_k, params_v, hkv, d):
+    torch = _torch()
+    _typed(torch.float32, params_k=params_k, params_v=params_v)
+    _contiguous(params_k=params_k, params_v=params_v)
+    for p in (params_k, params_v):
+        if p.numel() != hkv * 2 * d:
+            raise ValueError("rotation parameters are not [Hkv][d/4][8]")
+
+
+def _check_lens(lens, n, name):
+    torch = _torch()
+    _typed(torch.int32, **{name: lens})
+    _contiguous(**{name: lens})
+    if lens.numel() != n:
+        raise ValueError(f"{name} does not have {n} entries")
+
+
+def _check_out(out, like):
+    if out.shape != like.shape or out.dtype != like.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous, with the shape and dtype of q")
+
+
+class _on:
+    """The device made current for a launch, where it is not already."""
+
+    def __init__(self, dev):
+        torch = _torch()
+        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _scratch(workspace, nbytes, dev):
+    """The caller's workspace, or one from torch's allocator; and its bytes."""
+    if workspace is None:
+        return _torch().empty(nbytes, dtype=_torch().uint8, device=dev), nbytes
+    _contiguous(workspace=workspace)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def isoq_decode_window_workspace_size(B: int, Hq: int, Hkv: int, Tmax: int, d: int, window: int, n_sink: int) -> int:
+    return lib().isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink)
+
+
+def isoq_decode_prefix_workspace_size(B: int, Hq: int, Hkv: int, prefix_tokens: int, Tmax: int, d: int) -> int:
+    return lib().isoq_decode_prefix_workspace_size(B, Hq, Hkv, prefix_tokens, Tmax, d)
+
+
+def isoq_decode_attention_window(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, bits: int,
+                                 variant: int, window: int, n_sink: int = 0, scale: Optional[float] = None,
+                                 out=None, workspace=None, stream=None):
+    """Decode attention of q [B][Hq][d] over packed K/V, of which a row sees
+    its last ``window`` tokens and its first ``n_sink``; returns out (as q)."""
+    torch = _torch()
+    B, Hq, d = q.shape
+    b, Hkv, Tmax, _ = _check_cache(packed_k, packed_v, norms_k, norms_v, d, bits)
+    _contiguous(q=q, packed_k=packed_k, packed_v=packed_v, norms_k=norms_k, norms_v=norms_v)
+    if b != B:
+        raise ValueError("q and the cache differ in their batch")
+    _check_lens(seq_lens, B, "seq_lens")
+    _check_params(params_k, params_v, Hkv, d)
+    dev = _require_cuda(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, out, workspace)
+    out = torch.empty_like(q) if out is None else out
+    _check_out(out, q)
+    with _on(dev):
+        workspace, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink), dev)
+        st = lib().isoq_decode_attention_window(
+            _ptr(q), _dtype_code(q), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v), _ptr(seq_lens), B, Hq,
+            Hkv, Tmax, d, bits, variant, _ptr(params_k), _ptr(params_v), _scale(scale, d), window, n_sink, _ptr(out),
+            _ptr(workspace), ws, _stream(dev, stream))
+    _check(st, "isoq_decode_attention_window")
+    return out
+
+
+def isoq_prefill_attention_window(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, bits: int,
+                                  variant: int, window: int, n_sink: int = 0, scale: Optional[float] = None, out=None,
+                                  stream=None):
+    """Causal attention of q [B][Tq][Hq][d] over the packed cache that holds
+    the chunk, each query seeing the last ``window`` tokens up to its own and
+    the first ``n_sink``; returns out (as q)."""
+    torch = _torch()
+    B, Tq, Hq, d = q.shape
+    b, Hkv, Tmax, _ = _check_cache(packed_k, packed_v, norms_k, norms_v, d, bits)
+    _contiguous(q=q, packed_k=packed_k, packed_v=packed_v, norms_k=norms_k, norms_v=norms_v)
+    if b != B:
+        raise ValueError("q and the cache differ in their batch")
+    _check_lens(seq_lens, B, "seq_lens")
+    _check_params(params_k, params_v, Hkv, d)
+    dev = _require_cuda(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, out)
+    out = torch.empty_like(q) if out is None else out
+    _check_out(out, q)
+    with _on(dev):
+        st = lib().isoq_prefill_attention_window(
+            _ptr(q), _dtype_code(q), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v), _ptr(seq_lens), B, Tq,
+            Hq, Hkv, Tmax, d, bits, variant, _ptr(params_k), _ptr(params_v), _scale(scale, d), window, n_sink, _ptr(out),
+            _stream(dev, stream))
+    _check(st, "isoq_prefill_attention_window")
+    return out
+
+
+def isoq_decode_attention_prefix(q, prefix_k, prefix_v, prefix_norms_k, prefix_norms_v, prefix_len, packed_k, packed_v,
+                                 norms_k, norms_v, seq_lens, params_k, params_v, bits: int, variant: int,
+                                 scale: Optional[float] = None, out=None, workspace=None, stream=None):
+    """Decode attention of q [B][Hq][d] over a prefix [Hkv][Tp][d*bits/8] that
+    all rows share (its first ``prefix_len`` tokens, one int32 on the device)
+    and each row's own packed K/V; returns out (as q).  The prefix may be one
+    row of a larger cache: its KV heads may lie apart."""
+    torch = _torch()
+    B, Hq, d = q.shape
+    b, Hkv, Tmax, pb = _check_cache(packed_k, packed_v, norms_k, norms_v, d, bits)
+    _contiguous(q=q, packed_k=packed_k, packed_v=packed_v, norms_k=norms_k, norms_v=norms_v)
+    if b != B:
+        raise ValueError("q and the cache differ in their batch")
+    heads, Tp, _ = _check_cache(prefix_k, prefix_v, prefix_norms_k, prefix_norms_v, d, bits)
+    if heads != Hkv:
+        raise ValueError("the prefix and the cache differ in their KV heads")
+    apart = prefix_norms_k.stride(0) if Hkv > 1 else Tp
+    for t, row in ((prefix_k, pb), (prefix_v, pb), (prefix_norms_k, 1), (prefix_norms_v, 1)):
+        if Tp > 0 and ((Hkv > 1 and t.stride(0) != apart * row) or (Tp > 1 and t.stride(1) != row) or
+                       (t.dim() == 3 and t.stride(2) != 1)):
+            raise ValueError("the prefix's tokens must be contiguous, its KV heads equally far apart in all tensors")
+    _check_lens(seq_lens, B, "seq_lens")
+    _check_lens(prefix_len, 1, "prefix_len")
+    _check_params(params_k, params_v, Hkv, d)
+    dev = _require_cuda(q, prefix_k, prefix_v, prefix_norms_k, prefix_norms_v, prefix_len, packed_k, packed_v, norms_k,
+                        norms_v, seq_lens, params_k, params_v, out, workspace)
+    out = torch.empty_like(q) if out is None else out
+    _check_out(out, q)
+    with _on(dev):
+        workspace, ws = _scratch(workspace, isoq_decode_prefix_workspace_size(B, Hq, Hkv, Tp, Tmax, d), dev)
+        st = lib().isoq_decode_attention_prefix(
+            _ptr(q), _dtype_code(q), _ptr(prefix_k), _ptr(prefix_v), _ptr(prefix_norms_k), _ptr(prefix_norms_v),
+            _ptr(prefix_len), Tp, max(apart, Tp), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v),
+            _ptr(seq_lens), B, Hq, Hkv, Tmax, d, bits, variant, _ptr(params_k), _ptr(params_v), _scale(scale, d),
+            _ptr(out), _ptr(workspace), ws, _stream(dev, stream))
+    _check(st, "isoq_decode_attention_prefix")
+    return out
+
+
+def isoq_build_block_tables(seq_lens, new_lens, free_pages, block_table, page_tokens: int, n_slots: Optional[int] = None,
+                            free_head=None, slot_map=None, row_start=None, total_lens=None, pages_used=None, stream=None):
+    """Pages and slots of the tokens that a step adds to a paged cache: takes
+    the pages that the rows lack from ``free_pages`` (from ``free_head`` on) into
+    ``block_table`` [B][max_pages], in place; returns (slot_map [n_slots],
+    row_start [B + 1], total_lens [B], pages_used [1])."""
+    torch = _torch()
+    B, max_pages = block_table.shape
+    _check_lens(seq_lens, B, "seq_lens")
+    _check_lens(new_lens, B, "new_lens")
+    _typed(torch.int32, free_pages=free_pages, block_table=block_table, free_head=free_head, row_start=row_start,
+           total_lens=total_lens, pages_used=pages_used)
+    _typed(torch.int64, slot_map=slot_map)
+    _contiguous(free_pages=free_pages, block_table=block_table, slot_map=slot_map, row_start=row_start,
+                total_lens=total_lens, pages_used=pages_used)
+    if slot_map is None and n_slots is None:
+        raise ValueError("n_slots (or slot_map) says how many new tokens there may be")
+    dev = _require_cuda(seq_lens, new_lens, free_pages, block_table, free_head, slot_map, row_start, total_lens, pages_used)
+    if slot_map is None:
+        slot_map = torch.empty(n_slots, dtype=torch.int64, device=dev)
+    elif n_slots is not None and slot_map.numel() != n_slots:
+        raise ValueError("slot_map does not have n_slots entries")
+    if row_start is None:
+        row_start = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if total_lens is None:
+        total_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    if pages_used is None:
+        pages_used = torch.empty(1, dtype=torch.int32, device=dev)
+    for name, t, n in (("row_start", row_start, B + 1), ("total_lens", total_lens, B), ("pages_used", pages_used, 1)):
+        if t.numel() != n:
+            raise ValueError(f"{name} does not have {n} entries")
+    if free_head is not None and free_head.numel() != 1:
+        raise ValueError("free_head is one int32")
+    with _on(dev):
+        st = lib().isoq_build_block_tables(
+            _ptr(seq_lens), _ptr(new_lens), _ptr(free_pages), _ptr(free_head), free_pages.numel(), B, page_tokens,
+            max_pages, _ptr(block_table), slot_map.numel(), _ptr(slot_map), _ptr(row_start), _ptr(total_lens),
+            _ptr(pages_used), _stream(dev, stream))
+    _check(st, "isoq_build_block_tables")
+    return slot_map, row_start, total_lens, pages_used
+
+
+def isoq_paged_append(k_new, v_new, pages_k, pages_v, norms_k, norms_v, slot_map, params_k, params_v, bits: int,
+                      variant: int, stream=None):
+    """Compresses the new tokens k_new, v_new [N][Hkv][d] into the slots of
+    the pages [n_pages][Hkv][page_tokens][d*bits/8], in place; a negative slot's
+    token is skipped.  ``slot_map`` may be longer than N (a slot map of a fixed
+    shape): its first N entries count."""
+    torch = _torch()
+    N, Hkv, d = k_new.shape
+    n_pages, heads, P, _ = _check_cache(pages_k, pages_v, norms_k, norms_v, d, bits)
+    if heads != Hkv or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("the new K and V and the pages do not belong together")
+    _typed(torch.int64, slot_map=slot_map)
+    _contiguous(k_new=k_new, v_new=v_new, pages_k=pages_k, pages_v=pages_v, norms_k=norms_k, norms_v=norms_v,
+                slot_map=slot_map)
+    if slot_map.numel() < N:
+        raise ValueError("slot_map has fewer entries than there are new tokens")
+    _check_params(params_k, params_v, Hkv, d)
+    dev = _require_cuda(k_new, v_new, pages_k, pages_v, norms_k, norms_v, slot_map, params_k, params_v)
+    with _on(dev):
+        st = lib().isoq_paged_append(
+            _ptr(k_new), _ptr(v_new), _dtype_code(k_new), _ptr(pages_k), _ptr(pages_v), _ptr(norms_k), _ptr(norms_v),
+            _ptr(slot_map), N, Hkv, n_pages, P, d, bits, variant, _ptr(params_k), _ptr(params_v), _stream(dev, stream))
+    _check(st, "isoq_paged_append")
+
+
+def isoq_paged_decode_attention(q, pages_k, pages_v, norms_k, norms_v, block_table, seq_lens, params_k, params_v,
+                                bits: int, variant: int, max_len: Optional[int] = None, window: Optional[int] = None,
+                                n_sink: int = 0, scale: Optional[float] = None, out=None, workspace=None, stream=None):
+    """Decode attention of q [B][Hq][d] over the pages that ``block_table``
+    [B][max_pages] lists; ``max_len`` bounds the lengths (default: what the
+    table holds), ``window`` and ``n_sink`` as isoq_decode_attention_window
+    (default: all tokens).  Returns out (as q)."""
+    torch = _torch()
+    B, Hq, d = q.shape
+    n_pages, Hkv, P, _ = _check_cache(pages_k, pages_v, norms_k, norms_v, d, bits)
+    _typed(torch.int32, block_table=block_table)
+    _contiguous(q=q, pages_k=pages_k, pages_v=pages_v, norms_k=norms_k, norms_v=norms_v, block_table=block_table)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table is not [B][max_pages]")
+    max_pages = block_table.shape[1]
+    max_len = max_pages * P if max_len is None else max_len
+    window = max_len if window is None else window
+    _check_lens(seq_lens, B, "seq_lens")
+    _check_params(params_k, params_v, Hkv, d)
+    dev = _require_cuda(q, pages_k, pages_v, norms_k, norms_v, block_table, seq_lens, params_k, params_v, out, workspace)
+    out = torch.empty_like(q) if out is None else out
+    _check_out(out, q)
+    with _on(dev):
+        workspace, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, max_len, d, window, n_sink), dev)
+        st = lib().isoq_paged_decode_attention(
+            _ptr(q), _dtype_code(q), _ptr(pages_k), _ptr(pages_v), _ptr(norms_k), _ptr(norms_v), _ptr(block_table),
+            _ptr(seq_lens), B, Hq, Hkv, n_pages, P, max_pages, max_len, d, bits, variant, _ptr(params_k), _ptr(params_v),
+            _scale(scale, d), window, n_sink, _ptr(out), _ptr(workspace), ws, _stream(dev, stream))
+    _check(st, "isoq_paged_decode_attention")
+    return out

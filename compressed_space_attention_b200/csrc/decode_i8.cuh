@@ -68,6 +68,7 @@
 
 constexpr int kI8Warps = 4;
 constexpr int kI8Threads = 32 * kI8Warps;
+constexpr int kPagedChunkMax = 4096;     // tokens of one split through a block table
 constexpr int kBlk = 32;                 // tokens per ring stage (two 16-token MMA tiles)
 constexpr int kI8Stages = 2;             // per-warp ring depth
 constexpr int kCentroidIntMax = 16319;   // |C_k| bound that keeps Ch, 2 Cl in int8
@@ -241,6 +242,20 @@ __device__ __forceinline__ uint32_t pack_s8x4(int v0, int v1, int v2, int v3) {
 }
 
 
+// Row h of the CTA's query rows: its index [B][Hq], and its partial state in
+// split `split`.
+template <int MODE>
+__device__ __forceinline__ RowGroup cta_rows(const SplitArgs &a, int z) {
+  if constexpr (MODE == kSplitDense) return RowGroup{z, 0, a.group, false};
+  else return row_group(a, MODE, z);
+}
+
+template <int MODE>
+__device__ __forceinline__ long long state_slot(const SplitArgs &a, const RowGroup &g, int kvh, int h, int split) {
+  if constexpr (MODE == kSplitDense) return group_query(a, g, kvh, h) * a.n_splits + split;
+  else return group_slot(a, g, kvh, h, split);
+}
+
 // Query preparation, one CTA per (b, kvh): rotate the G queries once,
 // q~ = R_K q, and write for every lane of the split kernel the B-fragment
 // words of the fixed-point query Q = rint(q~ / qinv) = 2^14 Qh + 2^7 Qm + Ql
@@ -260,7 +275,10 @@ __device__ __forceinline__ uint32_t pack_s8x4(int v0, int v1, int v2, int v3) {
 // same to the bit), then 1/sqrt(d) and the block map on the lane's own 4-dim
 // blocks.  The part words go through shared memory once to their fragment
 // positions.
-template <int D, bool FULL, int GP>
+//
+// In the modes (SplitMode) other than kSplitDense blockIdx.y is a group of
+// query rows (RowGroup) instead of a batch row.
+template <int D, bool FULL, int GP, int MODE = kSplitDense>
 __global__ void __launch_bounds__(32 * GP) prep_i8_kernel(const SplitArgs a, float score_unit) {
   using C = I8Cfg<D, GP>;
   constexpr int E = D / 32, NQUAD = D / 4;
@@ -268,12 +286,13 @@ __global__ void __launch_bounds__(32 * GP) prep_i8_kernel(const SplitArgs a, flo
   __shared__ float qinv_s[8];
   const int kvh = blockIdx.x, b = blockIdx.y;
   const int tid = threadIdx.x, h = tid >> 5, lane = tid & 31;
-  const int G = a.group;
+  const RowGroup grp_rows = cta_rows<MODE>(a, b);
+  const int G = grp_rows.rows;
   pdl_launch_dependents();   // the split kernel may start its staging now
 
   float x[E];
   if (h < G) {
-    const __half *qp = static_cast<const __half *>(a.q) + (static_cast<long long>(b) * a.hq + kvh * G + h) * D + E * lane;
+    const __half *qp = static_cast<const __half *>(a.q) + group_query(a, grp_rows, kvh, h) * D + E * lane;
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(qp + e));
@@ -377,7 +396,15 @@ __global__ void __launch_bounds__(32 * GP) prep_i8_kernel(const SplitArgs a, flo
 // or one warp after the other into one buffer, a barrier each (for long
 // chunks, where the sliced form measured 0.7 % slower: it changes how the
 // main loop compiles).
-template <int D, bool FULL, int GP, bool SLICES>
+//
+// MODE (SplitMode): kSplitDense takes its tokens as one contiguous run.  The
+// others list the 32-token blocks that the query sees (SeenBlocks) and split
+// that list: the copies of a round follow it (a round that spans the gap
+// between sinks and window takes two runs; with pages, one copy per page and
+// tensor, issued by the lanes of one warp), and a block that is not seen
+// whole masks by token.  Tokens that are not seen carry score -inf and V norm
+// 0, whatever their codes and norms hold.
+template <int D, bool FULL, int GP, bool SLICES, int MODE = kSplitDense>
 __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
     split_i8_kernel(const SplitArgs a, const I8Lut lut, float out_scale) {
   using C = I8Cfg<D, GP>;
@@ -386,7 +413,12 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.group;
+  const RowGroup grp_rows = cta_rows<MODE>(a, b);
+  const int G = grp_rows.rows;
+  const bool over_prefix = MODE == kSplitPrefix && grp_rows.prefix;
+  const long long chunk = over_prefix ? a.chunk_p : a.chunk;
+  // The grid covers the longer of the two split counts.
+  if (MODE == kSplitPrefix && split >= (over_prefix ? a.n_splits_p : a.n_splits)) return;
 
   unsigned char *ring = smem;                       // [stage][round]
   float *scratch = reinterpret_cast<float *>(smem + kI8Warps * C::RING_BYTES);
@@ -397,25 +429,113 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
   uint32_t *done_cnt = reinterpret_cast<uint32_t *>(full_bar + kI8Stages);   // [stage]
   uint32_t *rounds_issued = done_cnt + kI8Stages;
 
-  int tlen = a.seq_lens[b];
-  tlen = tlen < 0 ? 0 : (tlen > a.tmax ? static_cast<int>(a.tmax) : tlen);
-  const long long t0 = static_cast<long long>(split) * a.chunk;
-  long long t1 = t0 + a.chunk;
+  constexpr bool LISTED = MODE != kSplitDense;   // tokens by a list of blocks
+  const int row = grp_rows.row;                  // cache row
+  const long long tmax = over_prefix ? a.prefix_max : a.tmax;
+  int tlen = over_prefix ? *a.prefix_len : a.seq_lens[row];
+  tlen = tlen < 0 ? 0 : (tlen > tmax ? static_cast<int>(tmax) : tlen);
+  const long long t0 = static_cast<long long>(split) * chunk;
+  long long t1 = t0 + chunk;
   if (t1 > tlen) t1 = tlen;
   const int n_tok = t1 > t0 ? static_cast<int>(t1 - t0) : 0;
-  const int n_blk = (n_tok + kBlk - 1) / kBlk;
+  SeenBlocks seen{};
+  int v0 = 0;   // the split's first place in the list
+  int n_blk = (n_tok + kBlk - 1) / kBlk;
+  if constexpr (LISTED) {
+    seen = seen_blocks(tlen, a.window, a.n_sink);   // kSplitPrefix: no window
+    const int per = static_cast<int>(chunk) / kBlk;
+    v0 = split * per;
+    n_blk = seen.n_blocks - v0;
+    n_blk = n_blk < 0 ? 0 : (n_blk > per ? per : n_blk);
+  }
+  auto block_at = [&](int v) { return v < seen.n_sink_blocks ? v : v - seen.n_sink_blocks + seen.first; };
   const int n_mine = n_blk > warp ? (n_blk - warp + kI8Warps - 1) / kI8Warps : 0;
 
   const long long pair = static_cast<long long>(b) * a.hkv + kvh;
-  const uint8_t *kb = a.packed_k + pair * a.tmax * C::PB;
-  const uint8_t *vb = a.packed_v + pair * a.tmax * C::PB;
-  const uint16_t *nkb = a.norms_k + pair * a.tmax;
-  const uint16_t *nvb = a.norms_v + pair * a.tmax;
+  const long long cache0 = MODE == kSplitDense ? pair * a.tmax
+                           : MODE == kSplitPaged ? 0   // pages: see issue
+                           : over_prefix         ? kvh * a.head_stride
+                                                 : (static_cast<long long>(row) * a.hkv + kvh) * a.tmax;
+  const uint8_t *kb = (over_prefix ? a.prefix_k : a.packed_k) + cache0 * C::PB;
+  const uint8_t *vb = (over_prefix ? a.prefix_v : a.packed_v) + cache0 * C::PB;
+  const uint16_t *nkb = (over_prefix ? a.prefix_nk : a.norms_k) + cache0;
+  const uint16_t *nvb = (over_prefix ? a.prefix_nv : a.norms_v) + cache0;
+
+  // kSplitPaged: the pages of the split's blocks, one entry per block, two
+  // where a page holds 16 tokens; -1 past the row's end.
+  __shared__ int page_of[MODE == kSplitPaged ? kPagedChunkMax / 16 : 1];
+  const int unit_shift = MODE == kSplitPaged && a.page_shift == 4 ? 1 : 0;
+  if constexpr (MODE == kSplitPaged) {
+    bool bad = false;
+    for (int u = tid; u < n_blk << unit_shift; u += kI8Threads) {
+      const int t = kBlk * block_at(v0 + (u >> unit_shift)) + 16 * (u & unit_shift);
+      int page = -1;
+      if (t < tlen) {
+        page = a.block_table[static_cast<long long>(row) * a.max_pages + (t >> a.page_shift)];
+        if (page < 0 || page >= a.n_pages) {   // reported; page 0 stands in
+          page = 0;
+          bad = true;
+        }
+      }
+      page_of[u] = page;
+    }
+    if (bad) atomicOr(&g_decode_error, kErrBadPage);
+    __syncthreads();
+  }
 
   // One thread issues the copies of round r (tokens 128 r .. 128 r + 127 of
   // the chunk) into stage r % kI8Stages.
   const int n_rounds = (n_blk + kI8Warps - 1) / kI8Warps;
   auto issue = [&](int r) {
+    if constexpr (MODE == kSplitPaged) {
+      // Every lane of one warp: lane (unit, tensor) copies one page's share
+      // of one tensor (16 or 32 tokens); whole shares, tokens past the end
+      // of the row among them, since a page is always there whole.
+      const int s = r % kI8Stages, u0 = kI8Warps * r << unit_shift;
+      int units = (n_blk << unit_shift) - u0;
+      units = units > kI8Warps << unit_shift ? kI8Warps << unit_shift : units;
+      const int ut = kBlk >> unit_shift;         // tokens of a unit
+      const int u = lane >> 2, which = lane & 3;
+      const int page = u < units ? page_of[u0 + u] : -1;
+      const int live = __popc(__ballot_sync(0xffffffffu, page >= 0 && which == 0));
+      unsigned char *st = ring + s * C::ROUND_BYTES;
+      if (lane == 0) {
+        *rounds_issued = static_cast<uint32_t>(r + 1);
+        mbar_arrive_expect_tx(&full_bar[s], static_cast<uint32_t>(live * ut * (2 * C::PB + 4)));
+      }
+      __syncwarp();
+      if (page >= 0) {
+        const int t = kBlk * block_at(v0 + kI8Warps * r + (u >> unit_shift)) + 16 * (u & unit_shift);
+        const long long at = ((static_cast<long long>(page) * a.hkv + kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+        if (which == 0) bulk_load(st + u * ut * C::PB, a.packed_k + at * C::PB, ut * C::PB, &full_bar[s]);
+        else if (which == 1) bulk_load(st + C::R_V + u * ut * C::PB, a.packed_v + at * C::PB, ut * C::PB, &full_bar[s]);
+        else if (which == 2) bulk_load(st + C::R_NK + u * ut * 2, a.norms_k + at, ut * 2, &full_bar[s]);
+        else bulk_load(st + C::R_NV + u * ut * 2, a.norms_v + at, ut * 2, &full_bar[s]);
+      }
+      return;
+    } else if constexpr (LISTED) {
+      const int s = r % kI8Stages, w0 = v0 + kI8Warps * r;
+      int nb = n_blk - kI8Warps * r;
+      nb = nb > kI8Warps ? kI8Warps : nb;
+      // The round's blocks as up to two runs of tokens.
+      int nb0 = seen.n_sink_blocks - w0;
+      nb0 = nb0 < 0 ? 0 : (nb0 > nb ? nb : nb0);
+      const int ta = kBlk * w0, tb = kBlk * block_at(w0 + nb0);
+      const int na = min(kBlk * nb0, tlen - ta) * (nb0 > 0), nt = nb > nb0 ? min(kBlk * (nb - nb0), tlen - tb) : 0;
+      const int na8 = (na + 7) & ~7, nt8 = (nt + 7) & ~7;
+      unsigned char *st = ring + s * C::ROUND_BYTES;
+      mbar_arrive_expect_tx(&full_bar[s], 2u * (na + nt) * C::PB + 4u * (na8 + nt8));
+      auto run = [&](int at, long long t, int n, int n8) {
+        bulk_load(st + at * C::PB, kb + t * C::PB, n * C::PB, &full_bar[s]);
+        bulk_load(st + C::R_V + at * C::PB, vb + t * C::PB, n * C::PB, &full_bar[s]);
+        bulk_load(st + C::R_NK + at * 2, nkb + t, 2 * n8, &full_bar[s]);
+        bulk_load(st + C::R_NV + at * 2, nvb + t, 2 * n8, &full_bar[s]);
+      };
+      if (na > 0) run(0, ta, na, na8);
+      if (nt > 0) run(kBlk * nb0, tb, nt, nt8);
+      *rounds_issued = static_cast<uint32_t>(r + 1);
+      return;
+    }
     const long long t = t0 + static_cast<long long>(r) * (kI8Warps * kBlk);
     int n = n_tok - r * (kI8Warps * kBlk);
     if (n > kI8Warps * kBlk) n = kI8Warps * kBlk;
@@ -436,7 +556,14 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
     }
     *rounds_issued = 0u;
     mbar_fence_init();
-    for (int r = 0; r < kI8Stages && r < n_rounds; ++r) issue(r);
+    if constexpr (MODE != kSplitPaged)
+      for (int r = 0; r < kI8Stages && r < n_rounds; ++r) issue(r);
+  }
+  if constexpr (MODE == kSplitPaged) {
+    if (warp == 0) {
+      __syncwarp();
+      for (int r = 0; r < kI8Stages && r < n_rounds; ++r) issue(r);
+    }
   }
   __syncthreads();   // every warp waits on the barriers thread 0 initialised
 
@@ -491,6 +618,7 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
     }
     int nvalid = n_tok - (warp + kI8Warps * i) * kBlk;
     nvalid = nvalid > kBlk ? kBlk : nvalid;
+    const unsigned vmask = LISTED ? seen_mask(seen, block_at(v0 + warp + kI8Warps * i)) : 0xFFFFFFFFu;
     const unsigned char *st = ring + s * C::ROUND_BYTES;
     const unsigned char *kc = st + warp * C::BLK_CODES;
     const unsigned char *vc = st + C::R_V + warp * C::BLK_CODES;
@@ -623,7 +751,7 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
       const float sk = lds_half(nk + 2 * lane);
       float svl = lds_half(nv + 2 * lane);
       float x0 = z0 * sk * qk0, x1 = z1 * sk * qk1;
-      if (nvalid < kBlk && lane >= nvalid) {   // the chunk's partial last block
+      if (LISTED ? !((vmask >> lane) & 1u) : nvalid < kBlk && lane >= nvalid) {   // not seen, or past the chunk's end
         x0 = x1 = -INFINITY;
         svl = 0.f;
       }
@@ -678,12 +806,12 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
         x[T][2 * hh + 1] = sc[T][2 * hh + 1] * sk * qk1;
       }
     }
-    if (nvalid < kBlk) {   // the chunk's partial last block (warp-uniform)
+    if (LISTED ? vmask != 0xFFFFFFFFu : nvalid < kBlk) {   // a block not seen whole, or the chunk's last (warp-uniform)
 #pragma unroll
       for (int T = 0; T < 2; ++T) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const bool ok = 16 * T + 8 * hh + g < nvalid;
+          const bool ok = LISTED ? (vmask >> (16 * T + 8 * hh + g)) & 1u : 16 * T + 8 * hh + g < nvalid;
           sv[T][hh] = ok ? sv[T][hh] : 0.f;
           x[T][2 * hh] = ok ? x[T][2 * hh] : -INFINITY;
           x[T][2 * hh + 1] = ok ? x[T][2 * hh + 1] : -INFINITY;
@@ -861,7 +989,21 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
     // round i is full (all four warps read stage s) and the fourth warp to
     // finish refills it; the counter's acquire-release add orders the other
     // warps' reads before that copy.
-    if (lane == 0 && kI8Warps * (i + kI8Stages) < n_blk) {
+    if constexpr (MODE == kSplitPaged) {
+      if (kI8Warps * (i + kI8Stages) < n_blk) {   // warp-uniform
+        uint32_t old = 0;
+        if (lane == 0)
+          asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;"
+                       : "=r"(old)
+                       : "r"(smem_u32(&done_cnt[s]))
+                       : "memory");
+        old = __shfl_sync(0xffffffffu, old, 0);
+        if ((old & (kI8Warps - 1)) == kI8Warps - 1) {
+          fence_proxy_async_smem();
+          issue(i + kI8Stages);
+        }
+      }
+    } else if (lane == 0 && kI8Warps * (i + kI8Stages) < n_blk) {
       uint32_t old;
       asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;"
                    : "=r"(old)
@@ -930,7 +1072,7 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
         const float mw = wm[w2 * 8 + h];
         f[w2] = mw == -INFINITY ? 0.f : exp2f(mw - mstar);
       }
-      const long long slot = (static_cast<long long>(b) * a.hq + kvh * G + h) * a.n_splits + split;
+      const long long slot = state_slot<MODE>(a, grp_rows, kvh, h, split);
       float *acc_out = a.ws_acc + slot * D;
       for (int i = tid; i < D; i += kI8Threads) {
         float sum = 0.f;
@@ -993,7 +1135,7 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
 
     // One partial state per query head: natural-log max, sum, acc (unscaled).
     for (int h = 0; h < G; ++h) {
-      const long long slot = (static_cast<long long>(b) * a.hq + kvh * G + h) * a.n_splits + split;
+      const long long slot = state_slot<MODE>(a, grp_rows, kvh, h, split);
       float *acc_out = a.ws_acc + slot * D;
       for (int i = tid; i < D; i += kI8Threads) acc_out[i] = scratch[h * D + i] * out_scale;
       if (tid == 0) {
@@ -1022,7 +1164,7 @@ inline int floor_div128(int x) { return x >= 0 ? x / 128 : -((-x + 127) / 128); 
 
 // S in [0.75, 1] * 16319 / c_max minimising the largest relative rounding
 // error of S c_k over the four positive 3-bit centroids (searched once).
-const I8Tables &i8_tables() {
+inline const I8Tables &i8_tables() {
   static I8Tables tb;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -1059,18 +1201,21 @@ const I8Tables &i8_tables() {
   return tb;
 }
 
-template <int D, bool FULL, int GP>
+template <int D, bool FULL, int GP, int MODE = kSplitDense>
 int launch_split_i8(const SplitArgs &a, cudaStream_t stream) {
   using C = I8Cfg<D, GP>;
   // The sliced warp merge for chunks up to 2048 tokens (see split_i8_kernel).
   const bool slices = a.chunk <= 2048;
-  auto kernel = slices ? split_i8_kernel<D, FULL, GP, true> : split_i8_kernel<D, FULL, GP, false>;
+  // (The rotation is the preparation's: one split kernel serves both variants
+  // in the modes other than kSplitDense.)
+  constexpr bool SF = MODE == kSplitDense ? FULL : true;
+  auto kernel = slices ? split_i8_kernel<D, SF, GP, true, MODE> : split_i8_kernel<D, SF, GP, false, MODE>;
   static bool configured = false;
   static std::mutex mu;
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!configured) {
-      for (auto k : {split_i8_kernel<D, FULL, GP, true>, split_i8_kernel<D, FULL, GP, false>}) {
+      for (auto k : {split_i8_kernel<D, SF, GP, true, MODE>, split_i8_kernel<D, SF, GP, false, MODE>}) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "decode i8: %s", cudaGetErrorString(e));
       }
@@ -1081,36 +1226,12 @@ int launch_split_i8(const SplitArgs &a, cudaStream_t stream) {
   const double unit = 1.0 / (tb.scale * std::sqrt(static_cast<double>(D)));
   const float score_unit = static_cast<float>(a.scale * unit * 1.4426950408889634);
   const float out_scale = static_cast<float>(unit);
-  dim3 grid(a.n_splits, a.hkv, a.batch);
+  const int z = MODE == kSplitDense ? a.batch : group_count(a, MODE);
+  dim3 grid(MODE == kSplitPrefix && a.n_splits_p > a.n_splits ? a.n_splits_p : a.n_splits, a.hkv, z);
   static_assert(C::QPREP_WORDS == decode_qprep_words(D), "prepared-query layout");
-  prep_i8_kernel<D, FULL, GP><<<dim3(a.hkv, a.batch), 32 * GP, 0, stream>>>(a, score_unit);
+  prep_i8_kernel<D, FULL, GP, MODE><<<dim3(a.hkv, z), 32 * GP, 0, stream>>>(a, score_unit);
   cudaError_t e = launch_pdl(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a, tb.lut, out_scale);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "decode i8 launch: %s", cudaGetErrorString(e));
   return ISOQ_OK;
-}
-
-// Float16 queries, 3-bit codes, d in {128, 256}, G <= 8, and chunks and
-// rows whose bulk copies start on 16-byte boundaries (the int32 PV sums cover
-// 16 tokens and the QK sums one token, so any chunk length is in range).
-bool i8_path_supported(int dtype, int d, int bits, const SplitArgs &a) {
-  return dtype == ISOQ_F16 && bits == 3 && (d == 128 || d == 256) && a.group <= 8 &&
-         a.tmax % 8 == 0 && a.chunk % kDecodeTokenQuantum == 0 &&
-         (reinterpret_cast<uintptr_t>(a.norms_k) & 15u) == 0 &&
-         (reinterpret_cast<uintptr_t>(a.norms_v) & 15u) == 0;
-}
-
-template <int D, bool FULL>
-int run_split_i8_d(const SplitArgs &a, cudaStream_t st) {
-  const int G = a.group;
-  if (G == 1) return launch_split_i8<D, FULL, 1>(a, st);
-  if (G == 2) return launch_split_i8<D, FULL, 2>(a, st);
-  if (G <= 4) return launch_split_i8<D, FULL, 4>(a, st);
-  return launch_split_i8<D, FULL, 8>(a, st);
-}
-
-int run_split_i8(int d, int variant, const SplitArgs &a, cudaStream_t st) {
-  if (d == 128)
-    return variant == ISOQ_FULL ? run_split_i8_d<128, true>(a, st) : run_split_i8_d<128, false>(a, st);
-  return variant == ISOQ_FULL ? run_split_i8_d<256, true>(a, st) : run_split_i8_d<256, false>(a, st);
 }

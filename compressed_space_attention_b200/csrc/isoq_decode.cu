@@ -35,88 +35,7 @@
 namespace isoq {
 namespace decode {
 
-using namespace isoq::dev;
-
-__device__ unsigned int g_decode_error = 0;
-
-// Launch with programmatic dependent launch: the kernel may start while the
-// previous kernel on the stream is still running (once that kernel's CTAs
-// have all started or signalled), and must execute griddepcontrol.wait
-// before reading anything the previous kernel writes.  Used only for
-// kernels whose predecessor is one of ours (prep -> split -> combine).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// Barrier over the threads taking part in a shared-memory rotation: the whole
-// CTA (bar_id 0 -> __syncthreads) or a named barrier over `nthreads` threads.
-__device__ __forceinline__ void rotation_sync(int bar_id, int nthreads) {
-  if (bar_id == 0)
-    __syncthreads();
-  else
-    named_barrier(bar_id, nthreads);
-}
-
-// Forward rotation q~ = R q of `nvec` vectors v[nvec][D] held in shared
-// memory, all sharing one head's parameters, by threads [0, nthreads): WHT
-// butterflies (stride h = 1 ... d/2) for all vectors per barrier, 1/sqrt(d),
-// then the per-block quaternion map.
-template <int D, bool FULL>
-__device__ void rotate_forward_smem(float *v, int nvec, const float *params_head, int tid,
-                                    int nthreads, int bar_id) {
-#pragma unroll 1
-  for (int h = 1; h < D; h <<= 1) {
-    for (int idx = tid; idx < nvec * (D / 2); idx += nthreads) {
-      const int g = idx / (D / 2), p = idx % (D / 2);
-      float *w = v + g * D;
-      const int i = (p / h) * 2 * h + (p % h);
-      const float a = w[i], b = w[i + h];
-      w[i] = a + b;
-      w[i + h] = a - b;
-    }
-    rotation_sync(bar_id, nthreads);
-  }
-  const float inv = rsqrtf(static_cast<float>(D));
-  for (int idx = tid; idx < nvec * (D / 4); idx += nthreads) {
-    const int g = idx / (D / 4), bi = idx % (D / 4);
-    float *w = v + g * D + 4 * bi;
-    const Quat x{w[0] * inv, w[1] * inv, w[2] * inv, w[3] * inv};
-    const Quat u = block_forward(load_quat(params_head + 8 * bi), load_quat(params_head + 8 * bi + 4), x, FULL);
-    w[0] = u.w;
-    w[1] = u.x;
-    w[2] = u.y;
-    w[3] = u.z;
-  }
-  rotation_sync(bar_id, nthreads);
-}
-
-template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+#include "decode_common.cuh"
 
 // Code of dimension i from a packed row read as 32-bit words (layout in
 // common.cuh).
@@ -353,6 +272,31 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
 #include "decode_append.cuh"
 #include "prefill.cuh"
 
+// Float16 queries, 3-bit codes, d in {128, 256}, G <= 8, and chunks and
+// rows whose bulk copies start on 16-byte boundaries (the int32 PV sums cover
+// 16 tokens and the QK sums one token, so any chunk length is in range).
+bool i8_path_supported(int dtype, int d, int bits, const SplitArgs &a) {
+  return dtype == ISOQ_F16 && bits == 3 && (d == 128 || d == 256) && a.group <= 8 &&
+         a.tmax % 8 == 0 && a.chunk % kDecodeTokenQuantum == 0 &&
+         (reinterpret_cast<uintptr_t>(a.norms_k) & 15u) == 0 &&
+         (reinterpret_cast<uintptr_t>(a.norms_v) & 15u) == 0;
+}
+
+template <int D, bool FULL>
+int run_split_i8_d(const SplitArgs &a, cudaStream_t st) {
+  const int G = a.group;
+  if (G == 1) return launch_split_i8<D, FULL, 1>(a, st);
+  if (G == 2) return launch_split_i8<D, FULL, 2>(a, st);
+  if (G <= 4) return launch_split_i8<D, FULL, 4>(a, st);
+  return launch_split_i8<D, FULL, 8>(a, st);
+}
+
+int run_split_i8(int d, int variant, const SplitArgs &a, cudaStream_t st) {
+  if (d == 128)
+    return variant == ISOQ_FULL ? run_split_i8_d<128, true>(a, st) : run_split_i8_d<128, false>(a, st);
+  return variant == ISOQ_FULL ? run_split_i8_d<256, true>(a, st) : run_split_i8_d<256, false>(a, st);
+}
+
 // ---------------------------------------------------------------------------
 // Host launchers
 // ---------------------------------------------------------------------------
@@ -423,8 +367,6 @@ int run_combine(int dtype, int d, int variant, const CombineArgs &a, cudaStream_
 #undef ISOQ_CD
 #undef ISOQ_CV
 }
-
-bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int validate_common(int dtype, int B, int Hq, int Hkv, int64_t Tmax, int d, int variant,
                     const void *ws, size_t ws_bytes) {
@@ -675,47 +617,12 @@ int isoq_prefill_attention(const void *q_dev, int dtype, const uint8_t *packed_k
                            const float *params_k_dev, const float *params_v_dev, float scale,
                            void *out_dev, isoq_stream_t stream) {
   clear_error();
-  if (d != 128 && d != 256) return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: d=%d (128 or 256)", d);
-  if (bits != 3) return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: bits=%d (3)", bits);
-  if (!supported_decode_variant(variant)) return set_error(ISOQ_ERR_UNSUPPORTED, "variant=%d", variant);
-  if (dtype != ISOQ_F16) return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: dtype=%d (float16 queries)", dtype);
-  if (B <= 0 || Tq < 0 || Hq <= 0 || Hkv <= 0 || Tmax <= 0)
-    return set_error(ISOQ_ERR_INVALID_ARG, "B, Hq, Hkv and Tmax must be positive, Tq >= 0");
-  if (Hq % Hkv) return set_error(ISOQ_ERR_INVALID_ARG, "Hq %% Hkv != 0");
-  const int G = Hq / Hkv;
-  if (G != 1 && G != 2 && G != 4 && G != 8)
-    return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: Hq/Hkv=%d (1, 2, 4 or 8)", G);
-  if (Tmax >= (1ll << 31) || B > 65535 || Hkv > 65535 || Tq > (1 << 24))
-    return set_error(ISOQ_ERR_INVALID_ARG, "shape too large");
-  if (Tmax % 8) return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: Tmax %% 8 != 0");
-  if (!q_dev || !packed_k_dev || !packed_v_dev || !norms_k_dev || !norms_v_dev || !seq_lens_dev ||
-      !params_k_dev || !params_v_dev || !out_dev)
-    return set_error(ISOQ_ERR_INVALID_ARG, "null pointer");
-  if (!decode::aligned(packed_k_dev, 16) || !decode::aligned(packed_v_dev, 16) ||
-      !decode::aligned(params_k_dev, 16) || !decode::aligned(params_v_dev, 16) ||
-      !decode::aligned(q_dev, 4) || !decode::aligned(out_dev, 4) || !decode::aligned(norms_k_dev, 2) ||
-      !decode::aligned(norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4))
-    return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
-  if (!std::isfinite(scale)) return set_error(ISOQ_ERR_INVALID_ARG, "scale is not finite");
-  if (Tq == 0) return ISOQ_OK;
   decode::PrefillArgs a{};
-  a.q = q_dev;
-  a.packed_k = packed_k_dev;
-  a.packed_v = packed_v_dev;
-  a.norms_k = norms_k_dev;
-  a.norms_v = norms_v_dev;
-  a.seq_lens = seq_lens_dev;
-  a.params_k = params_k_dev;
-  a.params_v = params_v_dev;
-  a.out = out_dev;
-  a.tmax = Tmax;
-  a.batch = B;
-  a.tq = Tq;
-  a.hq = Hq;
-  a.hkv = Hkv;
-  a.group = G;
-  a.score_unit = static_cast<float>(scale * 1.4426950408889634);
-  return decode::run_prefill(d, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
+  const int st = decode::prefill_args(q_dev, dtype, packed_k_dev, packed_v_dev, norms_k_dev, norms_v_dev, seq_lens_dev,
+                                      B, Tq, Hq, Hkv, Tmax, d, bits, variant, params_k_dev, params_v_dev, scale,
+                                      out_dev, &a);
+  if (st || Tq == 0) return st;
+  return decode::run_prefill<false>(d, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,511 @@
+// Serving attention on the packed cache: decode under a sliding window with
+// sink tokens, decode of a batch that shares a prefix, the paged cache (block
+// tables, append, decode), and windowed chunked prefill.
+//
+// Decode runs as query preparation, split and combine, the launches of
+// isoq_decode_attention: the integer tensor-core split (decode_i8.cuh) for
+// float16 queries and 3-bit codes at d = 128 and 256, the CUDA-core split
+// (serve_any.cuh) for everything else.  A split covers a run of the list of
+// 32-token blocks that the query sees.
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <mutex>
+
+#include "common.cuh"
+#include "tcgen05.cuh"
+#include "decode.h"
+#include "internal.h"
+
+namespace isoq {
+namespace decode {
+
+#include "decode_common.cuh"
+#include "decode_i8.cuh"
+#include "prefill.cuh"
+#include "serve_any.cuh"
+#include "paged.cuh"
+
+// ---------------------------------------------------------------------------
+// Plans
+// ---------------------------------------------------------------------------
+
+inline int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+inline int64_t div_up(int64_t n, int64_t m) { return (n + m - 1) / m; }
+
+// Query heads of one CTA: a KV head's group, or even shares of at most 8.
+inline int row_share(int rows) { return static_cast<int>(div_up(rows, div_up(rows, 8))); }
+
+// Most 32-token blocks that a decode query sees of a row of up to `tmax`
+// tokens.
+inline int64_t most_blocks(int64_t tmax, int64_t window, int64_t n_sink) {
+  const int64_t all = div_up(tmax, 32), near = div_up(window, 32) + 1, sink = div_up(n_sink, 32);
+  return near < all && sink < all && near + sink < all ? near + sink : all;
+}
+
+// Tokens per split for `ctas` row groups of `tokens` listed tokens each.
+inline int64_t serve_chunk(int64_t ctas, int64_t tokens) {
+  static constexpr int64_t kChunks[] = {4096, 2048, 1536, 1024, 768, 512, 256, 128};
+  constexpr int64_t kSms = 148, kSlots = 4, kCtaCost = 160;
+  int64_t best_chunk = kChunks[0], best_cost = -1;
+  for (const int64_t c : kChunks) {
+    const int64_t splits = div_up(tokens, c);
+    int64_t m = div_up(ctas * splits, kSms), phases10 = 0;
+    const int64_t full = m / kSlots;
+    phases10 = full * (10 * kSlots + 7);
+    if (m % kSlots) phases10 += 10 * (m % kSlots) + 7;
+    const int64_t cost = phases10 * ((c < tokens ? c : tokens) + kCtaCost);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best_chunk = c;
+    }
+  }
+  return best_chunk;
+}
+
+struct DecodePlan {
+  int share, groups;                 // query heads per CTA, CTAs per (b, kvh)
+  int share_p, groups_p;             // the same over the prefix's rows
+  int64_t chunk, chunk_p;
+  int splits, splits_p;
+  int64_t acc_bytes, prep_bytes;     // workspace: partial states; prepared queries
+};
+
+// prefix_max < 0: no prefix.  The list of a row is cut into the same splits
+// whatever its length.
+DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int64_t window, int64_t n_sink) {
+  DecodePlan p{};
+  const int G = Hq / Hkv;
+  p.share = row_share(G);
+  p.groups = static_cast<int>(div_up(G, p.share));
+  const int64_t tokens = 32 * most_blocks(tmax, window, n_sink);
+  p.chunk = serve_chunk(static_cast<int64_t>(B) * Hkv * p.groups, tokens);
+  p.splits = static_cast<int>(div_up(tokens, p.chunk));
+  int64_t prep_rows = static_cast<int64_t>(B) * p.groups;
+  if (prefix_max >= 0) {
+    const int64_t rows = static_cast<int64_t>(B) * G;
+    p.share_p = row_share(static_cast<int>(rows < 8 ? rows : 8));
+    p.groups_p = static_cast<int>(div_up(rows, p.share_p));
+    const int64_t tp = 32 * div_up(prefix_max, 32);
+    p.chunk_p = serve_chunk(static_cast<int64_t>(Hkv) * p.groups_p, tp > 0 ? tp : 32);
+    p.splits_p = static_cast<int>(div_up(tp, p.chunk_p));
+    prep_rows += p.groups_p;
+  }
+  p.acc_bytes = round256(static_cast<int64_t>(B) * Hq * (p.splits + p.splits_p) * (d + 2) * 4);
+  const int64_t i8 = prep_rows * Hkv * decode_qprep_words(d) * 4, any = static_cast<int64_t>(B) * Hq * d * 4;
+  p.prep_bytes = round256(i8 > any ? i8 : any);
+  return p;
+}
+
+// ---------------------------------------------------------------------------
+// Checks and launches
+// ---------------------------------------------------------------------------
+
+int check_decode(int dtype, int B, int Hq, int Hkv, int64_t tmax, int d, int bits, int variant, int64_t window,
+                 int64_t n_sink, float scale) {
+  if (!supported_d(d)) return set_error(ISOQ_ERR_UNSUPPORTED, "d=%d not supported", d);
+  if (!supported_bits(bits)) return set_error(ISOQ_ERR_UNSUPPORTED, "bits=%d not supported", bits);
+  if (!supported_decode_variant(variant)) return set_error(ISOQ_ERR_UNSUPPORTED, "variant=%d", variant);
+  if (!supported_dtype(dtype)) return set_error(ISOQ_ERR_UNSUPPORTED, "dtype=%d", dtype);
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || tmax <= 0)
+    return set_error(ISOQ_ERR_INVALID_ARG, "B, Hq, Hkv and the longest row must be positive");
+  if (Hq % Hkv) return set_error(ISOQ_ERR_INVALID_ARG, "Hq %% Hkv != 0");
+  if (Hq / Hkv > kMaxGroup) return set_error(ISOQ_ERR_UNSUPPORTED, "Hq/Hkv > %d", kMaxGroup);
+  if (tmax >= (1ll << 31) || B > 16384 || Hkv > 65535 || Hq > (1 << 24))
+    return set_error(ISOQ_ERR_INVALID_ARG, "shape too large");
+  if (window < 0 || n_sink < 0) return set_error(ISOQ_ERR_INVALID_ARG, "window and n_sink must not be negative");
+  if (!std::isfinite(scale)) return set_error(ISOQ_ERR_INVALID_ARG, "scale is not finite");
+  return ISOQ_OK;
+}
+
+int check_workspace(const void *ws, size_t bytes, const DecodePlan &p) {
+  if (!ws) return set_error(ISOQ_ERR_INVALID_ARG, "workspace is NULL");
+  if (!aligned(ws, 256)) return set_error(ISOQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const size_t need = static_cast<size_t>(p.acc_bytes + p.prep_bytes);
+  if (bytes < need) return set_error(ISOQ_ERR_INVALID_ARG, "workspace too small: %zu < %zu", bytes, need);
+  return ISOQ_OK;
+}
+
+// The page size's logarithm; -1: not a power of two from 16 to 256.
+int page_shift_of(int page_tokens) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_tokens == 1 << s) return s;
+  return -1;
+}
+
+inline int clamp31(int64_t n) { return n > 0x7FFFFFFF ? 0x7FFFFFFF : static_cast<int>(n); }
+
+template <int D, bool FULL, int GP>
+int run_i8_mode(const SplitArgs &a, cudaStream_t st) {
+  if (a.mode == kSplitPaged) return launch_split_i8<D, FULL, GP, kSplitPaged>(a, st);
+  if (a.mode == kSplitPrefix) return launch_split_i8<D, FULL, GP, kSplitPrefix>(a, st);
+  return launch_split_i8<D, FULL, GP, kSplitWindow>(a, st);
+}
+
+template <int D, bool FULL>
+int run_i8_rows(const SplitArgs &a, cudaStream_t st) {
+  const int rows = a.mode == kSplitPrefix && a.zrow_size_p > a.zrow_size ? a.zrow_size_p : a.zrow_size;
+  if (rows == 1) return run_i8_mode<D, FULL, 1>(a, st);
+  if (rows == 2) return run_i8_mode<D, FULL, 2>(a, st);
+  if (rows <= 4) return run_i8_mode<D, FULL, 4>(a, st);
+  return run_i8_mode<D, FULL, 8>(a, st);
+}
+
+// The bulk copies of the integer split start on 16-byte boundaries: rows of
+// a multiple of 8 tokens, norms aligned to 16 bytes.
+bool i8_cache(const uint16_t *nk, const uint16_t *nv, int64_t room) {
+  return room % 8 == 0 && aligned(nk, 16) && aligned(nv, 16);
+}
+
+// Preparation, split and combine over the partial states in `workspace`.
+int run_decode(SplitArgs &a, const DecodePlan &p, int dtype, int d, int bits, int variant, bool i8, const float *params_v,
+               void *out, void *workspace, cudaStream_t st) {
+  variant = block_map_variant(variant);
+  a.group = a.hq / a.hkv;
+  a.n_splits = p.splits;
+  a.n_splits_p = p.splits_p;
+  a.slot_stride = p.splits + p.splits_p;
+  a.slot_off = p.splits_p;
+  a.chunk = p.chunk;
+  a.chunk_p = p.chunk_p;
+  a.zrow_size = p.share;
+  a.n_zrows = p.groups;
+  a.zrow_size_p = p.share_p;
+  a.n_zrows_p = p.groups_p;
+  a.ws_acc = static_cast<float *>(workspace);
+  a.ws_ml = reinterpret_cast<float2 *>(a.ws_acc + static_cast<int64_t>(a.batch) * a.hq * a.slot_stride * d);
+  unsigned char *prep = static_cast<unsigned char *>(workspace) + p.acc_bytes;
+  a.ws_qprep = reinterpret_cast<uint32_t *>(prep);
+  a.ws_qrot = reinterpret_cast<float *>(prep);
+  CodebookF32 cb;
+  codebook_f32(d, bits, &cb);
+  for (int j = 0; j < 16; ++j) a.centroid[j] = j < cb.levels ? cb.centroid[j] : 0.f;
+  int e;
+  if (i8 && dtype == ISOQ_F16 && bits == 3 && (d == 128 || d == 256)) {
+    if (d == 128)
+      e = variant == ISOQ_FULL ? run_i8_rows<128, true>(a, st) : run_i8_rows<128, false>(a, st);
+    else
+      e = variant == ISOQ_FULL ? run_i8_rows<256, true>(a, st) : run_i8_rows<256, false>(a, st);
+  } else {
+    e = run_prep_rotate(dtype, d, variant, a, st);
+    if (e == ISOQ_OK) e = run_split_any(d, bits, a, st);
+  }
+  if (e) return e;
+  CombineArgs c;
+  c.params_v = params_v;
+  c.out = out;
+  c.ws_acc = a.ws_acc;
+  c.ws_ml = a.ws_ml;
+  c.batch = a.batch;
+  c.hq = a.hq;
+  c.group = a.group;
+  c.n_splits = a.slot_stride;
+  return run_combine(dtype, d, variant, c, st);
+}
+
+// Whether two byte ranges share a byte.
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
+}  // namespace decode
+}  // namespace isoq
+
+using namespace isoq;
+
+extern "C" {
+
+size_t isoq_decode_window_workspace_size(int B, int Hq, int Hkv, int64_t Tmax, int d, int64_t window, int64_t n_sink) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Tmax <= 0 || Tmax >= (1ll << 31) || !supported_d(d) || Hq % Hkv || window < 0 ||
+      n_sink < 0)
+    return 0;
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, -1, d, window, n_sink);
+  return static_cast<size_t>(p.acc_bytes + p.prep_bytes);
+}
+
+size_t isoq_decode_prefix_workspace_size(int B, int Hq, int Hkv, int64_t prefix_tokens, int64_t Tmax, int d) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Tmax <= 0 || Tmax >= (1ll << 31) || prefix_tokens < 0 ||
+      prefix_tokens >= (1ll << 31) || !supported_d(d) || Hq % Hkv)
+    return 0;
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0);
+  return static_cast<size_t>(p.acc_bytes + p.prep_bytes);
+}
+
+int isoq_decode_attention_window(const void *q_dev, int dtype, const uint8_t *packed_k_dev,
+                                 const uint8_t *packed_v_dev, const uint16_t *norms_k_dev,
+                                 const uint16_t *norms_v_dev, const int32_t *seq_lens_dev, int B, int Hq, int Hkv,
+                                 int64_t Tmax, int d, int bits, int variant, const float *params_k_dev,
+                                 const float *params_v_dev, float scale, int64_t window, int64_t n_sink,
+                                 void *out_dev, void *workspace_dev, size_t workspace_bytes, isoq_stream_t stream) {
+  clear_error();
+  int st = decode::check_decode(dtype, B, Hq, Hkv, Tmax, d, bits, variant, window, n_sink, scale);
+  if (st) return st;
+  if (!q_dev || !packed_k_dev || !packed_v_dev || !norms_k_dev || !norms_v_dev || !seq_lens_dev || !params_k_dev ||
+      !params_v_dev || !out_dev)
+    return set_error(ISOQ_ERR_INVALID_ARG, "null pointer");
+  if (!decode::aligned(q_dev, 16) || !decode::aligned(packed_k_dev, 16) || !decode::aligned(packed_v_dev, 16) ||
+      !decode::aligned(params_k_dev, 16) || !decode::aligned(params_v_dev, 16) || !decode::aligned(out_dev, 16) ||
+      !decode::aligned(norms_k_dev, 2) || !decode::aligned(norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4))
+    return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, -1, d, window, n_sink);
+  st = decode::check_workspace(workspace_dev, workspace_bytes, p);
+  if (st) return st;
+  decode::SplitArgs a{};
+  a.mode = decode::kSplitWindow;
+  a.q = q_dev;
+  a.packed_k = packed_k_dev;
+  a.packed_v = packed_v_dev;
+  a.norms_k = norms_k_dev;
+  a.norms_v = norms_v_dev;
+  a.seq_lens = seq_lens_dev;
+  a.params_k = params_k_dev;
+  a.tmax = Tmax;
+  a.batch = B;
+  a.hq = Hq;
+  a.hkv = Hkv;
+  a.scale = scale;
+  a.window = decode::clamp31(window);
+  a.n_sink = decode::clamp31(n_sink);
+  return decode::run_decode(a, p, dtype, d, bits, variant, decode::i8_cache(norms_k_dev, norms_v_dev, Tmax),
+                            params_v_dev, out_dev, workspace_dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *prefix_k_dev,
+                                 const uint8_t *prefix_v_dev, const uint16_t *prefix_norms_k_dev,
+                                 const uint16_t *prefix_norms_v_dev, const int32_t *prefix_len_dev,
+                                 int64_t prefix_tokens, int64_t prefix_head_stride, const uint8_t *packed_k_dev,
+                                 const uint8_t *packed_v_dev, const uint16_t *norms_k_dev,
+                                 const uint16_t *norms_v_dev, const int32_t *seq_lens_dev, int B, int Hq, int Hkv,
+                                 int64_t Tmax, int d, int bits, int variant, const float *params_k_dev,
+                                 const float *params_v_dev, float scale, void *out_dev, void *workspace_dev,
+                                 size_t workspace_bytes, isoq_stream_t stream) {
+  clear_error();
+  int st = decode::check_decode(dtype, B, Hq, Hkv, Tmax, d, bits, variant, 0, 0, scale);
+  if (st) return st;
+  if (prefix_tokens < 0 || prefix_tokens >= (1ll << 31))
+    return set_error(ISOQ_ERR_INVALID_ARG, "prefix_tokens=%lld", static_cast<long long>(prefix_tokens));
+  if (prefix_head_stride < prefix_tokens)
+    return set_error(ISOQ_ERR_INVALID_ARG, "prefix_head_stride < prefix_tokens");
+  if (!q_dev || !packed_k_dev || !packed_v_dev || !norms_k_dev || !norms_v_dev || !seq_lens_dev || !params_k_dev ||
+      !params_v_dev || !out_dev || !prefix_len_dev ||
+      (prefix_tokens > 0 && (!prefix_k_dev || !prefix_v_dev || !prefix_norms_k_dev || !prefix_norms_v_dev)))
+    return set_error(ISOQ_ERR_INVALID_ARG, "null pointer");
+  if (!decode::aligned(q_dev, 16) || !decode::aligned(packed_k_dev, 16) || !decode::aligned(packed_v_dev, 16) ||
+      !decode::aligned(prefix_k_dev, 16) || !decode::aligned(prefix_v_dev, 16) || !decode::aligned(params_k_dev, 16) ||
+      !decode::aligned(params_v_dev, 16) || !decode::aligned(out_dev, 16) || !decode::aligned(norms_k_dev, 2) ||
+      !decode::aligned(norms_v_dev, 2) || !decode::aligned(prefix_norms_k_dev, 2) ||
+      !decode::aligned(prefix_norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4) || !decode::aligned(prefix_len_dev, 4))
+    return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0);
+  st = decode::check_workspace(workspace_dev, workspace_bytes, p);
+  if (st) return st;
+  decode::SplitArgs a{};
+  a.mode = decode::kSplitPrefix;
+  a.q = q_dev;
+  a.packed_k = packed_k_dev;
+  a.packed_v = packed_v_dev;
+  a.norms_k = norms_k_dev;
+  a.norms_v = norms_v_dev;
+  a.seq_lens = seq_lens_dev;
+  a.params_k = params_k_dev;
+  a.tmax = Tmax;
+  a.batch = B;
+  a.hq = Hq;
+  a.hkv = Hkv;
+  a.scale = scale;
+  a.window = 0x7FFFFFFF;
+  a.n_sink = 0;
+  a.prefix_k = prefix_k_dev;
+  a.prefix_v = prefix_v_dev;
+  a.prefix_nk = prefix_norms_k_dev;
+  a.prefix_nv = prefix_norms_v_dev;
+  a.prefix_len = prefix_len_dev;
+  a.prefix_max = prefix_tokens;
+  a.head_stride = prefix_head_stride;
+  // A copy of norms is rounded up to 8 tokens: within the room of the last
+  // KV head only where the prefix's tokens are a multiple of 8.
+  const bool i8 = decode::i8_cache(norms_k_dev, norms_v_dev, Tmax) &&
+                  decode::i8_cache(prefix_norms_k_dev, prefix_norms_v_dev, prefix_head_stride) && prefix_tokens % 8 == 0;
+  return decode::run_decode(a, p, dtype, d, bits, variant, i8, params_v_dev, out_dev, workspace_dev,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+int isoq_paged_decode_attention(const void *q_dev, int dtype, const uint8_t *pages_k_dev, const uint8_t *pages_v_dev,
+                                const uint16_t *norms_k_dev, const uint16_t *norms_v_dev,
+                                const int32_t *block_table_dev, const int32_t *seq_lens_dev, int B, int Hq, int Hkv,
+                                int n_pages, int page_tokens, int max_pages, int64_t max_len, int d, int bits,
+                                int variant, const float *params_k_dev, const float *params_v_dev, float scale,
+                                int64_t window, int64_t n_sink, void *out_dev, void *workspace_dev,
+                                size_t workspace_bytes, isoq_stream_t stream) {
+  clear_error();
+  const int shift = decode::page_shift_of(page_tokens);
+  if (shift < 0)
+    return set_error(ISOQ_ERR_UNSUPPORTED, "page_tokens=%d (16, 32, 64, 128 or 256)", page_tokens);
+  if (n_pages <= 0 || max_pages <= 0) return set_error(ISOQ_ERR_INVALID_ARG, "n_pages and max_pages must be positive");
+  int st = decode::check_decode(dtype, B, Hq, Hkv, max_len, d, bits, variant, window, n_sink, scale);
+  if (st) return st;
+  if (max_len > static_cast<int64_t>(max_pages) * page_tokens)
+    return set_error(ISOQ_ERR_INVALID_ARG, "max_len is more than the block table holds");
+  if (!q_dev || !pages_k_dev || !pages_v_dev || !norms_k_dev || !norms_v_dev || !block_table_dev || !seq_lens_dev ||
+      !params_k_dev || !params_v_dev || !out_dev)
+    return set_error(ISOQ_ERR_INVALID_ARG, "null pointer");
+  if (!decode::aligned(q_dev, 16) || !decode::aligned(pages_k_dev, 16) || !decode::aligned(pages_v_dev, 16) ||
+      !decode::aligned(params_k_dev, 16) || !decode::aligned(params_v_dev, 16) || !decode::aligned(out_dev, 16) ||
+      !decode::aligned(norms_k_dev, 2) || !decode::aligned(norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4) ||
+      !decode::aligned(block_table_dev, 4))
+    return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, max_len, -1, d, window, n_sink);
+  st = decode::check_workspace(workspace_dev, workspace_bytes, p);
+  if (st) return st;
+  decode::SplitArgs a{};
+  a.mode = decode::kSplitPaged;
+  a.q = q_dev;
+  a.packed_k = pages_k_dev;
+  a.packed_v = pages_v_dev;
+  a.norms_k = norms_k_dev;
+  a.norms_v = norms_v_dev;
+  a.seq_lens = seq_lens_dev;
+  a.params_k = params_k_dev;
+  a.tmax = max_len;
+  a.batch = B;
+  a.hq = Hq;
+  a.hkv = Hkv;
+  a.scale = scale;
+  a.window = decode::clamp31(window);
+  a.n_sink = decode::clamp31(n_sink);
+  a.block_table = block_table_dev;
+  a.page_shift = shift;
+  a.max_pages = max_pages;
+  a.n_pages = n_pages;
+  return decode::run_decode(a, p, dtype, d, bits, variant, decode::i8_cache(norms_k_dev, norms_v_dev, 8),
+                            params_v_dev, out_dev, workspace_dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int isoq_prefill_attention_window(const void *q_dev, int dtype, const uint8_t *packed_k_dev,
+                                  const uint8_t *packed_v_dev, const uint16_t *norms_k_dev,
+                                  const uint16_t *norms_v_dev, const int32_t *seq_lens_dev, int B, int Tq, int Hq,
+                                  int Hkv, int64_t Tmax, int d, int bits, int variant, const float *params_k_dev,
+                                  const float *params_v_dev, float scale, int64_t window, int64_t n_sink,
+                                  void *out_dev, isoq_stream_t stream) {
+  clear_error();
+  decode::PrefillArgs a{};
+  const int st = decode::prefill_args(q_dev, dtype, packed_k_dev, packed_v_dev, norms_k_dev, norms_v_dev, seq_lens_dev,
+                                      B, Tq, Hq, Hkv, Tmax, d, bits, variant, params_k_dev, params_v_dev, scale,
+                                      out_dev, &a);
+  if (st) return st;
+  if (window < 0 || n_sink < 0) return set_error(ISOQ_ERR_INVALID_ARG, "window and n_sink must not be negative");
+  if (Tq == 0) return ISOQ_OK;
+  a.window = decode::clamp31(window);
+  a.n_sink = decode::clamp31(n_sink);
+  return decode::run_prefill<true>(d, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int isoq_build_block_tables(const int32_t *seq_lens_dev, const int32_t *new_lens_dev, const int32_t *free_pages_dev,
+                            const int32_t *free_head_dev, int n_free, int B, int page_tokens, int max_pages,
+                            int32_t *block_table_dev, int64_t n_slots, int64_t *slot_map_dev, int32_t *row_start_dev,
+                            int32_t *total_lens_dev, int32_t *pages_used_dev, isoq_stream_t stream) {
+  clear_error();
+  const int shift = decode::page_shift_of(page_tokens);
+  if (shift < 0)
+    return set_error(ISOQ_ERR_UNSUPPORTED, "page_tokens=%d (16, 32, 64, 128 or 256)", page_tokens);
+  if (B <= 0 || max_pages <= 0 || n_free < 0 || n_slots < 0)
+    return set_error(ISOQ_ERR_INVALID_ARG, "B and max_pages must be positive, n_free and n_slots not negative");
+  if (n_slots >= (1ll << 31)) return set_error(ISOQ_ERR_INVALID_ARG, "n_slots too large");
+  if (!seq_lens_dev || !new_lens_dev || (!free_pages_dev && n_free > 0) || !block_table_dev ||
+      (!slot_map_dev && n_slots > 0) || !row_start_dev || !total_lens_dev || !pages_used_dev)
+    return set_error(ISOQ_ERR_INVALID_ARG, "null pointer");
+  if (!decode::aligned(seq_lens_dev, 4) || !decode::aligned(new_lens_dev, 4) || !decode::aligned(free_pages_dev, 4) ||
+      !decode::aligned(free_head_dev, 4) || !decode::aligned(block_table_dev, 4) || !decode::aligned(slot_map_dev, 8) ||
+      !decode::aligned(row_start_dev, 4) || !decode::aligned(total_lens_dev, 4) || !decode::aligned(pages_used_dev, 4))
+    return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
+  // Every CTA reads the inputs while others write: no output may share memory
+  // with an input or another output.
+  struct { const void *p; int64_t n; } r[] = {
+      {block_table_dev, 4ll * B * max_pages}, {slot_map_dev, 8 * n_slots}, {row_start_dev, 4ll * B + 4},
+      {total_lens_dev, 4ll * B}, {pages_used_dev, 4}, {seq_lens_dev, 4ll * B}, {new_lens_dev, 4ll * B},
+      {free_pages_dev, 4ll * n_free}, {free_head_dev, free_head_dev ? 4 : 0}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 9; ++j)
+      if (decode::overlap(r[i].p, r[i].n, r[j].p, r[j].n))
+        return set_error(ISOQ_ERR_INVALID_ARG, "an output overlaps an input or another output");
+  decode::TableArgs a;
+  a.seq_lens = seq_lens_dev;
+  a.new_lens = new_lens_dev;
+  a.free_pages = free_pages_dev;
+  a.free_head = free_head_dev;
+  a.block_table = block_table_dev;
+  a.slot_map = reinterpret_cast<long long *>(slot_map_dev);
+  a.row_start = row_start_dev;
+  a.total_lens = total_lens_dev;
+  a.pages_used = pages_used_dev;
+  a.n_slots = n_slots;
+  a.batch = B;
+  a.n_free = n_free;
+  a.max_pages = max_pages;
+  a.page_shift = shift;
+  const int64_t ctas = decode::div_up(n_slots, decode::kTableTokens);
+  decode::block_tables_kernel<<<static_cast<unsigned>(ctas > 1 ? ctas : 1), decode::kTableThreads, 0,
+                                reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "block tables launch: %s", cudaGetErrorString(e));
+}
+
+int isoq_paged_append(const void *k_new_dev, const void *v_new_dev, int dtype, uint8_t *pages_k_dev,
+                      uint8_t *pages_v_dev, uint16_t *norms_k_dev, uint16_t *norms_v_dev, const int64_t *slot_map_dev,
+                      int64_t N, int Hkv, int n_pages, int page_tokens, int d, int bits, int variant,
+                      const float *params_k_dev, const float *params_v_dev, isoq_stream_t stream) {
+  clear_error();
+  if (!supported_d(d)) return set_error(ISOQ_ERR_UNSUPPORTED, "d=%d not supported", d);
+  if (!supported_bits(bits)) return set_error(ISOQ_ERR_UNSUPPORTED, "bits=%d not supported", bits);
+  if (!supported_decode_variant(variant)) return set_error(ISOQ_ERR_UNSUPPORTED, "variant=%d", variant);
+  if (!supported_dtype(dtype)) return set_error(ISOQ_ERR_UNSUPPORTED, "dtype=%d", dtype);
+  const int shift = decode::page_shift_of(page_tokens);
+  if (shift < 0)
+    return set_error(ISOQ_ERR_UNSUPPORTED, "page_tokens=%d (16, 32, 64, 128 or 256)", page_tokens);
+  if (N < 0 || Hkv <= 0 || n_pages <= 0)
+    return set_error(ISOQ_ERR_INVALID_ARG, "Hkv and n_pages must be positive, N >= 0");
+  if (Hkv > 65535 || N >= (1ll << 31) || N * Hkv >= (1ll << 32)) return set_error(ISOQ_ERR_INVALID_ARG, "shape too large");
+  if (N == 0) return ISOQ_OK;
+  if (!k_new_dev || !v_new_dev || !pages_k_dev || !pages_v_dev || !norms_k_dev || !norms_v_dev || !slot_map_dev ||
+      !params_k_dev || !params_v_dev)
+    return set_error(ISOQ_ERR_INVALID_ARG, "null pointer");
+  if (!decode::aligned(k_new_dev, 16) || !decode::aligned(v_new_dev, 16) || !decode::aligned(pages_k_dev, 16) ||
+      !decode::aligned(pages_v_dev, 16) || !decode::aligned(params_k_dev, 16) || !decode::aligned(params_v_dev, 16) ||
+      !decode::aligned(norms_k_dev, 2) || !decode::aligned(norms_v_dev, 2) || !decode::aligned(slot_map_dev, 8))
+    return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
+  decode::PagedAppendArgs a{};
+  a.k_new = k_new_dev;
+  a.v_new = v_new_dev;
+  a.pages_k = pages_k_dev;
+  a.pages_v = pages_v_dev;
+  a.norms_k = norms_k_dev;
+  a.norms_v = norms_v_dev;
+  a.slot_map = reinterpret_cast<const long long *>(slot_map_dev);
+  a.params_k = params_k_dev;
+  a.params_v = params_v_dev;
+  a.n_vec = N * Hkv;
+  a.n_rows = static_cast<long long>(n_pages) << shift;
+  a.hkv = Hkv;
+  a.page_shift = shift;
+  const int half = 1 << (bits - 1);
+  isoq_make_codebook(d, bits, nullptr, a.thr64);
+  for (int k = 0; k < half; ++k) a.thr[k] = static_cast<float>(a.thr64[half - 1 + k]);
+  return decode::run_paged_append(dtype, d, bits, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+__attribute__((visibility("hidden"))) int isoq_detail_take_serve_error(cudaStream_t stream, unsigned *out) {
+  unsigned zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(out, decode::g_decode_error, sizeof(unsigned), 0, cudaMemcpyDeviceToHost,
+                                            stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess && *out)
+    e = cudaMemcpyToSymbolAsync(decode::g_decode_error, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "error word: %s", cudaGetErrorString(e));
+}
+
+}  // extern "C"

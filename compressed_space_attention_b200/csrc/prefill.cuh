@@ -70,6 +70,7 @@ struct PrefillArgs {
   float out_unit;                 // 1 / (alpha * d)
   uint32_t lut_lo0, lut_lo1, lut_hi0, lut_hi1;   // float16 alpha c_k, low / high bytes
   uint32_t res_lo0, res_lo1, res_hi0, res_hi1;   // float16 alpha c_k - fp16(alpha c_k), low / high bytes
+  int window, n_sink;             // WIN: tokens j > p - window or j < n_sink only
 };
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -201,7 +202,11 @@ __device__ __forceinline__ void tc_expand(const TcCodes<D> &c, unsigned char *ti
   }
 }
 
-template <typename T, int D, bool FULL, int GP>
+// WIN: a sliding window with sink tokens.  The query at position p sees j <= p
+// with j > p - window or j < n_sink.  The CTA's tiles are the sink tiles, then
+// those from the first row's window on; a tile that some row of a warp does
+// not see whole is masked by column.
+template <typename T, int D, bool FULL, int GP, bool WIN = false>
 __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_kernel(const PrefillArgs a) {
   using C = TcCfg<D>;
   constexpr int BQ = kTcRows / GP;
@@ -239,7 +244,26 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   if (tq0 + BQ > a.tq) p_last = pos_base + a.tq - 1;
   int tend = p_last + 1 < len ? p_last + 1 : len;
   if (tend < 0) tend = 0;
-  const int n_tiles = (tend + kTcTok - 1) / kTcTok;
+  int n_tiles = (tend + kTcTok - 1) / kTcTok;
+  // WIN: tiles [0, n_sink_tiles), then from win_tile on.
+  int n_sink_tiles = 0, win_tile = 0;
+  if constexpr (WIN) {
+    const int sink = a.n_sink < tend ? a.n_sink : tend;
+    int lo = p_first >= a.window ? p_first - a.window + 1 : 0;   // the first row's window begins here
+    if (lo > tend) lo = tend;
+    if (lo > sink) {
+      const int all = n_tiles;
+      n_sink_tiles = (sink + kTcTok - 1) / kTcTok;
+      win_tile = lo / kTcTok > n_sink_tiles ? lo / kTcTok : n_sink_tiles;
+      n_tiles = n_sink_tiles + (all > win_tile ? all - win_tile : 0);
+    }
+  }
+  auto tile_t0 = [&](int j) {
+    if constexpr (WIN)
+      return kTcTok * (j < n_sink_tiles ? j : j - n_sink_tiles + win_tile);
+    else
+      return kTcTok * j;
+  };
 
   const long long pair = static_cast<long long>(b) * a.hkv + kvh;
   const uint8_t *kb = a.packed_k + pair * a.tmax * C::PB;
@@ -253,13 +277,13 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   TcCodes<D> kc, vc;
   uint16_t nrm = 0;
   auto fetch_norm = [&](int j) {
-    const int t0 = j * kTcTok, tok = tid & (kTcTok - 1);
+    const int t0 = tile_t0(j), tok = tid & (kTcTok - 1);
     nrm = (tid < 2 * kTcTok && t0 + tok < tend) ? __ldg(((tid < kTcTok) ? nkb : nvb) + t0 + tok)
                                                 : static_cast<uint16_t>(0);
   };
   if (n_tiles > 0) {
-    tc_fetch<D>(kc, kb, 0, tend, tid);
-    tc_fetch<D>(vc, vb, 0, tend, tid);
+    tc_fetch<D>(kc, kb, tile_t0(0), tend, tid);
+    tc_fetch<D>(vc, vb, tile_t0(0), tend, tid);
     fetch_norm(0);
   }
 
@@ -327,7 +351,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   };
   auto stage_qk = [&](int j) {
     tc_expand<D, true>(kc, kt, klt, a, tid);
-    if (j + 1 < n_tiles) tc_fetch<D>(kc, kb, (j + 1) * kTcTok, tend, tid);
+    if (j + 1 < n_tiles) tc_fetch<D>(kc, kb, tile_t0(j + 1), tend, tid);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -350,6 +374,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   const int r = 32 * sub + lane;                              // this thread's row / TMEM lane
   const int pr = p_first + r / GP;
   const int pw_min = p_first + (32 * sub) / GP;
+  const int pw_max = p_first + (32 * sub + 31) / GP;
   constexpr int HC = kTcTok / 2;                               // score columns per thread
   constexpr int OH = D / 2;                                    // output columns per thread
   float mx = -INFINITY;
@@ -364,7 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     ++qk_issued;
   }
   for (int it = 0; it < n_tiles; ++it) {
-    const int t0 = it * kTcTok;
+    const int t0 = tile_t0(it);
     // QK(it) must be complete: its S buffer is read below and the K tile is
     // free.  Every thread waits on the mbarrier itself, so no block barrier
     // follows: a wait that gave up is recorded in fail_s[it % 2], which all
@@ -416,6 +441,16 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
       for (int j = 0; j < HC; ++j)
         if (c0 + j > pr || c0 + j >= tend) x[j] = -INFINITY;
     }
+    if constexpr (WIN) {
+      // Some row of the warp pair has left part of this tile behind, and the
+      // tile is not all sinks.
+      if (pw_max >= a.window && t0 <= pw_max - a.window && t0 + kTcTok > a.n_sink) {
+        const int behind = pr >= a.window ? pr - a.window : -1;   // the row's last token behind its window
+#pragma unroll
+        for (int j = 0; j < HC; ++j)
+          if (c0 + j <= behind && c0 + j >= a.n_sink) x[j] = -INFINITY;
+      }
+    }
     float tmx = -INFINITY;
 #pragma unroll
     for (int j = 0; j < HC; ++j) tmx = fmaxf(tmx, x[j]);
@@ -466,6 +501,10 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
         l2 = f2_add(l2, p2);
         const ulonglong2 n = nv4[j >> 2];
         f2_unpack(f2_mul(p2, (k & 1) ? n.y : n.x), p0, p1);
+        if constexpr (WIN) {   // a token that is not seen weighs nothing, whatever its norm holds
+          p0 = x[j] == -INFINITY ? 0.f : p0;
+          p1 = x[j + 1] == -INFINITY ? 0.f : p1;
+        }
         const __half2 h = __floats2half2_rn(p0, p1);
         const float2 hf = __half22float2(h);
         phi[4 * c + k] = *reinterpret_cast<const uint32_t *>(&h);
@@ -490,7 +529,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     }
     tc_expand<D, false>(vc, vt, nullptr, a, tid);
-    if (it + 1 < n_tiles) tc_fetch<D>(vc, vb, (it + 1) * kTcTok, tend, tid);
+    if (it + 1 < n_tiles) tc_fetch<D>(vc, vb, tile_t0(it + 1), tend, tid);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -578,10 +617,10 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
 }
 
-template <typename T, int D, bool FULL, int GP>
+template <typename T, int D, bool FULL, int GP, bool WIN>
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
   using C = TcCfg<D>;
-  auto kernel = prefill_tc_kernel<T, D, FULL, GP>;
+  auto kernel = prefill_tc_kernel<T, D, FULL, GP, WIN>;
   static bool configured = false;
   static std::mutex mu;
   {
@@ -658,23 +697,24 @@ inline const PfTables &pf_tables() {
   return tb;
 }
 
-template <typename T, int D, bool FULL>
+template <typename T, int D, bool FULL, bool WIN>
 int run_prefill_g(const PrefillArgs &a, cudaStream_t st) {
   switch (a.group) {
-    case 1: return launch_prefill_tc<T, D, FULL, 1>(a, st);
-    case 2: return launch_prefill_tc<T, D, FULL, 2>(a, st);
-    case 4: return launch_prefill_tc<T, D, FULL, 4>(a, st);
-    default: return launch_prefill_tc<T, D, FULL, 8>(a, st);
+    case 1: return launch_prefill_tc<T, D, FULL, 1, WIN>(a, st);
+    case 2: return launch_prefill_tc<T, D, FULL, 2, WIN>(a, st);
+    case 4: return launch_prefill_tc<T, D, FULL, 4, WIN>(a, st);
+    default: return launch_prefill_tc<T, D, FULL, 8, WIN>(a, st);
   }
 }
 
-template <typename T>
+template <typename T, bool WIN>
 int run_prefill_t(int d, int variant, const PrefillArgs &a, cudaStream_t st) {
   if (d == 128)
-    return variant == ISOQ_FULL ? run_prefill_g<T, 128, true>(a, st) : run_prefill_g<T, 128, false>(a, st);
-  return variant == ISOQ_FULL ? run_prefill_g<T, 256, true>(a, st) : run_prefill_g<T, 256, false>(a, st);
+    return variant == ISOQ_FULL ? run_prefill_g<T, 128, true, WIN>(a, st) : run_prefill_g<T, 128, false, WIN>(a, st);
+  return variant == ISOQ_FULL ? run_prefill_g<T, 256, true, WIN>(a, st) : run_prefill_g<T, 256, false, WIN>(a, st);
 }
 
+template <bool WIN>
 int run_prefill(int d, int variant, PrefillArgs a, cudaStream_t st) {
   const PfTables &tb = pf_tables();
   a.lut_lo0 = tb.lo0;
@@ -687,5 +727,53 @@ int run_prefill(int d, int variant, PrefillArgs a, cudaStream_t st) {
   a.res_hi1 = tb.rhi1;
   a.out_unit = static_cast<float>(1.0 / (tb.alpha * d));
   a.score_unit = static_cast<float>(a.score_unit / (tb.alpha * std::sqrt(static_cast<double>(d))));
-  return run_prefill_t<__half>(d, variant, a, st);
+  return run_prefill_t<__half, WIN>(d, variant, a, st);
+}
+
+// Checks the arguments of a prefill entry point and fills in the kernel's.
+inline int prefill_args(const void *q_dev, int dtype, const uint8_t *packed_k_dev, const uint8_t *packed_v_dev,
+                        const uint16_t *norms_k_dev, const uint16_t *norms_v_dev, const int32_t *seq_lens_dev, int B,
+                        int Tq, int Hq, int Hkv, int64_t Tmax, int d, int bits, int variant,
+                        const float *params_k_dev, const float *params_v_dev, float scale, void *out_dev,
+                        PrefillArgs *out) {
+  if (d != 128 && d != 256) return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: d=%d (128 or 256)", d);
+  if (bits != 3) return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: bits=%d (3)", bits);
+  if (!supported_decode_variant(variant)) return set_error(ISOQ_ERR_UNSUPPORTED, "variant=%d", variant);
+  if (dtype != ISOQ_F16) return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: dtype=%d (float16 queries)", dtype);
+  if (B <= 0 || Tq < 0 || Hq <= 0 || Hkv <= 0 || Tmax <= 0)
+    return set_error(ISOQ_ERR_INVALID_ARG, "B, Hq, Hkv and Tmax must be positive, Tq >= 0");
+  if (Hq % Hkv) return set_error(ISOQ_ERR_INVALID_ARG, "Hq %% Hkv != 0");
+  const int G = Hq / Hkv;
+  if (G != 1 && G != 2 && G != 4 && G != 8)
+    return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: Hq/Hkv=%d (1, 2, 4 or 8)", G);
+  if (Tmax >= (1ll << 31) || B > 65535 || Hkv > 65535 || Tq > (1 << 24))
+    return set_error(ISOQ_ERR_INVALID_ARG, "shape too large");
+  if (Tmax % 8) return set_error(ISOQ_ERR_UNSUPPORTED, "prefill: Tmax %% 8 != 0");
+  if (!q_dev || !packed_k_dev || !packed_v_dev || !norms_k_dev || !norms_v_dev || !seq_lens_dev ||
+      !params_k_dev || !params_v_dev || !out_dev)
+    return set_error(ISOQ_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(packed_k_dev, 16) || !aligned(packed_v_dev, 16) ||
+      !aligned(params_k_dev, 16) || !aligned(params_v_dev, 16) ||
+      !aligned(q_dev, 4) || !aligned(out_dev, 4) || !aligned(norms_k_dev, 2) ||
+      !aligned(norms_v_dev, 2) || !aligned(seq_lens_dev, 4))
+    return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
+  if (!std::isfinite(scale)) return set_error(ISOQ_ERR_INVALID_ARG, "scale is not finite");
+  PrefillArgs &a = *out;
+  a.q = q_dev;
+  a.packed_k = packed_k_dev;
+  a.packed_v = packed_v_dev;
+  a.norms_k = norms_k_dev;
+  a.norms_v = norms_v_dev;
+  a.seq_lens = seq_lens_dev;
+  a.params_k = params_k_dev;
+  a.params_v = params_v_dev;
+  a.out = out_dev;
+  a.tmax = Tmax;
+  a.batch = B;
+  a.tq = Tq;
+  a.hq = Hq;
+  a.hkv = Hkv;
+  a.group = G;
+  a.score_unit = static_cast<float>(scale * 1.4426950408889634);
+  return ISOQ_OK;
 }

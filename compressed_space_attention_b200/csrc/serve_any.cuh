@@ -1,0 +1,422 @@
+// CUDA-core split of the serving attention: any query dtype, d and bits, any
+// group, any alignment that the entry points take.  Included by
+// isoq_serve.cu inside namespace isoq::decode.
+//
+// Per query row: z_j = s^K_j <q~, c[K_j]> scale over the tokens it sees, one
+// pass with the running reference maximum and sum of the softmax, and
+// acc += p_j s^V_j c[V_j], all in float32 and in the rotated domain; one
+// partial state (m, l, acc[d]) per query row and split, merged by
+// combine_kernel.
+//
+// A CTA's four warps take the split's 32-token blocks in turn, up to RG query
+// rows at once, so that one unpacking of a code serves all of them.  For the
+// scores a lane is a token: it reads its packed row from shared memory 16
+// bytes at a time (row stride an odd number of 16-byte units: no bank
+// conflicts), looks each code up in a table of (c, c) pairs and multiplies it
+// with the query rows, two rows per f32x2 instruction, the query values
+// broadcast from shared memory.  For the values a lane is d / 32 dimensions
+// and the loop runs over the tokens, their weights broadcast.  The next block
+// arrives by 16-byte asynchronous copies (two stages per warp).
+//
+// Bound: issue slots.  Per token, 4 dimensions and RG = 8 rows the score
+// loop issues about 34 instructions (16 f32x2, 12 shared-memory loads), the
+// value loop as many.
+
+constexpr int kAnyWarps = 4;
+constexpr int kAnyThreads = 32 * kAnyWarps;
+
+template <int D, int BITS, int RG>
+struct AnyCfg {
+  static constexpr int PB = D * BITS / 8;
+  static constexpr int RS = ((PB / 16) | 1) * 16;           // row stride in shared memory
+  static constexpr int STAGE = 2 * 32 * RS;                 // K rows, V rows of a block
+  static constexpr int OFF_Q = 2 * kAnyWarps * STAGE;       // [D][RG] rotated queries
+  static constexpr int OFF_W = OFF_Q + D * RG * 4;          // [warp][32][RG] weights
+  static constexpr int OFF_TAB = OFF_W + kAnyWarps * 32 * RG * 4;   // [16] (c, c)
+  static constexpr int OFF_ML = OFF_TAB + 16 * 8;           // [warp][RG] (m, l)
+  static constexpr int SMEM = OFF_ML + kAnyWarps * RG * 8;
+  static_assert(kAnyWarps * RG * D * 4 <= OFF_Q, "the warps' accumulators fit the stages");
+};
+
+// Codes 4 quad .. + 3 of a packed row (32-bit words) as four 4-bit fields.
+template <int BITS>
+__device__ __forceinline__ uint32_t quad_fields(const uint32_t *w, int quad) {
+  if constexpr (BITS == 2) {
+    uint32_t x = (w[quad >> 2] >> (8 * (quad & 3))) & 0xFFu;
+    x = (x | (x << 4)) & 0x0F0Fu;
+    return (x | (x << 2)) & 0x3333u;
+  } else if constexpr (BITS == 4) {
+    return (w[quad >> 1] >> (16 * (quad & 1))) & 0xFFFFu;
+  } else {
+    const uint32_t *g = w + 3 * (quad >> 3);
+    const int q = quad & 7;
+    const uint32_t w0 = g[0], w1 = g[1], w2 = g[2];
+    const uint32_t body = (q < 2 ? w0 : (q < 4 ? w1 : w2)) & 0x77777777u;
+    const uint32_t tail = ((w0 & 0x88888888u) >> 3) + ((w1 & 0x88888888u) >> 2) + ((w2 & 0x88888888u) >> 1);
+    return ((q < 6 ? body : tail) >> (16 * (q & 1))) & 0x7777u;
+  }
+}
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Rotated queries q~ = R_K q scale log2(e), one warp per query row: the
+// Walsh-Hadamard stages h < E inside the lane, the others by shuffles, then
+// 1 / sqrt(d) and the block maps (the order of prep_i8_kernel).
+template <typename T, int D, bool FULL>
+__global__ void __launch_bounds__(128) prep_rotate_kernel(const SplitArgs a) {
+  constexpr int E = D / 32;
+  pdl_launch_dependents();
+  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= static_cast<long long>(a.batch) * a.hq) return;
+  const int kvh = static_cast<int>(r % a.hq) / a.group;
+  const T *q = static_cast<const T *>(a.q) + r * D + E * lane;
+  float x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = to_f32<T>(q[e]);
+#pragma unroll
+  for (int hs = 1; hs < E; hs <<= 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (!(e & hs)) {
+        const float u = x[e], v = x[e + hs];
+        x[e] = u + v;
+        x[e + hs] = u - v;
+      }
+    }
+  }
+#pragma unroll
+  for (int lm = 1; lm < 32; lm <<= 1) {
+    const bool upper = (lane & lm) != 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float o = __shfl_xor_sync(0xffffffffu, x[e], lm);
+      x[e] = upper ? o - x[e] : x[e] + o;
+    }
+  }
+  const float inv = rsqrtf(static_cast<float>(D));
+  const float sc = a.scale * 1.4426950408889634f;
+  const float *prm = a.params_k + static_cast<size_t>(kvh) * 2 * D;
+  float *out = a.ws_qrot + r * D + E * lane;
+#pragma unroll
+  for (int u = 0; u < E / 4; ++u) {
+    const int bi = (E / 4) * lane + u;
+    const Quat v{x[4 * u] * inv, x[4 * u + 1] * inv, x[4 * u + 2] * inv, x[4 * u + 3] * inv};
+    const Quat y = block_forward(load_quat(prm + 8 * bi), load_quat(prm + 8 * bi + 4), v, FULL);
+    *reinterpret_cast<float4 *>(out + 4 * u) = make_float4(y.w * sc, y.x * sc, y.y * sc, y.z * sc);
+  }
+}
+
+template <int D, int BITS, int RG>
+__global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs a) {
+  using C = AnyCfg<D, BITS, RG>;
+  constexpr int PB = C::PB, RS = C::RS, KD = D / 32, RP = RG / 2;
+  extern __shared__ __align__(128) unsigned char smem[];
+  float *qs = reinterpret_cast<float *>(smem + C::OFF_Q);
+  unsigned char *tab = smem + C::OFF_TAB;
+  float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+  const int split = blockIdx.x, kvh = blockIdx.y, z = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool paged = a.mode == kSplitPaged;
+  const RowGroup grp = row_group(a, a.mode, z);
+  const int row = grp.row, rows = grp.rows;
+  const long long chunk = grp.prefix ? a.chunk_p : a.chunk;
+  // The grid covers the longer of the two split counts (kSplitPrefix).
+  if (split >= (grp.prefix ? a.n_splits_p : a.n_splits)) return;
+  const uint8_t *pk = grp.prefix ? a.prefix_k : a.packed_k, *pv = grp.prefix ? a.prefix_v : a.packed_v;
+  const uint16_t *nk = grp.prefix ? a.prefix_nk : a.norms_k, *nv = grp.prefix ? a.prefix_nv : a.norms_v;
+  if (tid < 16) *reinterpret_cast<float2 *>(tab + 8 * tid) = make_float2(a.centroid[tid], a.centroid[tid]);
+
+  const long long tmax = grp.prefix ? a.prefix_max : a.tmax;
+  int tlen = grp.prefix ? *a.prefix_len : a.seq_lens[row];
+  tlen = tlen < 0 ? 0 : (tlen > tmax ? static_cast<int>(tmax) : tlen);
+  const SeenBlocks seen = seen_blocks(tlen, a.window, a.n_sink);   // kSplitPrefix: no window
+  const int per = static_cast<int>(chunk) / 32, v0 = split * per;
+  int n_blk = seen.n_blocks - v0;
+  n_blk = n_blk < 0 ? 0 : (n_blk > per ? per : n_blk);
+  const long long cache0 = paged ? 0 : grp.prefix ? kvh * a.head_stride : (static_cast<long long>(row) * a.hkv + kvh) * a.tmax;
+
+  // Cache row of token t (the same for 16 tokens from a multiple of 16 on,
+  // plus t mod 16).  A page index out of range is reported; page 0 stands in.
+  auto row16 = [&](int t) -> long long {
+    if (!paged) return cache0 + t;
+    int page = a.block_table[static_cast<long long>(row) * a.max_pages + (t >> a.page_shift)];
+    if (page < 0 || page >= a.n_pages) {
+      atomicOr(&g_decode_error, kErrBadPage);
+      page = 0;
+    }
+    return ((static_cast<long long>(page) * a.hkv + kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
+  };
+  unsigned char *stage = smem + warp * 2 * C::STAGE;
+  // Copies of block v's rows below tlen into stage s, and this lane's norms.
+  uint16_t nk_next = 0, nv_next = 0;
+  auto fetch = [&](int v, int s) {
+    const int block = v < seen.n_sink_blocks ? v : v - seen.n_sink_blocks + seen.first;
+    const int t0 = 32 * block, n = tlen - t0 < 32 ? tlen - t0 : 32;
+    const long long ra = row16(t0), rb = n > 16 ? (paged ? row16(t0 + 16) : ra + 16) : 0;
+    unsigned char *dk = stage + s * C::STAGE, *dv = dk + 32 * RS;
+    for (int i = lane; i < n * (PB / 16); i += 32) {
+      const int t = i / (PB / 16), p = 16 * (i % (PB / 16));
+      const long long src = (t < 16 ? ra + t : rb + t - 16) * PB + p;
+      cp_async16(dk + t * RS + p, pk + src);
+      cp_async16(dv + t * RS + p, pv + src);
+    }
+    nk_next = nv_next = 0;
+    if (lane < n) {
+      const long long at = lane < 16 ? ra + lane : rb + lane - 16;
+      nk_next = nk[at];
+      nv_next = nv[at];
+    }
+  };
+  if (warp < n_blk) fetch(v0 + warp, 0);
+  cp_async_commit();
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the rotated queries
+  pdl_launch_dependents();
+  for (int i = tid; i < RG * D; i += kAnyThreads) {
+    const int h = i / D, e = i % D;
+    qs[e * RG + h] = h < rows ? a.ws_qrot[group_query(a, grp, kvh, h) * D + e] : 0.f;
+  }
+  __syncthreads();
+
+  uint64_t acc[KD][RP];
+  float m[RG], l[RG];
+#pragma unroll
+  for (int k = 0; k < KD; ++k)
+#pragma unroll
+    for (int r = 0; r < RP; ++r) acc[k][r] = 0ull;
+#pragma unroll
+  for (int r = 0; r < RG; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+  }
+  float *wts = reinterpret_cast<float *>(smem + C::OFF_W) + warp * 32 * RG;
+
+  int it = 0;
+  for (int bi = warp; bi < n_blk; bi += kAnyWarps, ++it) {
+    const int s = it & 1, v = v0 + bi;
+    const float sk = __half2float(__ushort_as_half(nk_next)), svr = __half2float(__ushort_as_half(nv_next));
+    if (bi + kAnyWarps < n_blk) fetch(v + kAnyWarps, s ^ 1);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncwarp();
+    const unsigned char *kc = stage + s * C::STAGE, *vc = kc + 32 * RS;
+    const int block = v < seen.n_sink_blocks ? v : v - seen.n_sink_blocks + seen.first;
+    const unsigned mask = seen_mask(seen, block);
+    const bool ok = (mask >> lane) & 1u;
+
+    // ---- scores: this lane's token against the query rows ----
+    uint64_t dot[RP];
+#pragma unroll
+    for (int r = 0; r < RP; ++r) dot[r] = 0ull;
+#pragma unroll 1
+    for (int seg = 0; seg < D / 128; ++seg) {
+      constexpr int W = 4 * BITS;   // words of 128 codes
+      uint32_t w[W];
+#pragma unroll
+      for (int p = 0; p < BITS; ++p) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(kc + lane * RS + seg * (16 * BITS) + 16 * p);
+        w[4 * p] = u.x;
+        w[4 * p + 1] = u.y;
+        w[4 * p + 2] = u.z;
+        w[4 * p + 3] = u.w;
+      }
+      const float *qd = qs + seg * 128 * RG;
+#pragma unroll
+      for (int quad = 0; quad < 32; ++quad) {
+        const uint32_t f = quad_fields<BITS>(w, quad);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t off = e == 0 ? (f << 3) & 0x78u : (f >> (4 * e - 3)) & 0x78u;
+          const uint64_t c = *reinterpret_cast<const uint64_t *>(tab + off);
+          const float *qe = qd + (4 * quad + e) * RG;
+          if constexpr (RG >= 4) {
+#pragma unroll
+            for (int r = 0; r < RG / 4; ++r) {
+              const ulonglong2 qv = *reinterpret_cast<const ulonglong2 *>(qe + 4 * r);
+              dot[2 * r] = f2_fma(c, qv.x, dot[2 * r]);
+              dot[2 * r + 1] = f2_fma(c, qv.y, dot[2 * r + 1]);
+            }
+          } else {
+            dot[0] = f2_fma(c, *reinterpret_cast<const uint64_t *>(qe), dot[0]);
+          }
+        }
+      }
+    }
+    // ---- softmax (log2 domain); the reference maximum moves only when a
+    // score passes it by 8, so p <= 2^8 ----
+    float x[RG];
+    bool over = false;
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      f2_unpack(dot[r], x[2 * r], x[2 * r + 1]);
+      x[2 * r] = ok ? x[2 * r] * sk : -INFINITY;
+      x[2 * r + 1] = ok ? x[2 * r + 1] * sk : -INFINITY;
+      over |= x[2 * r] > m[2 * r] + 8.f || x[2 * r + 1] > m[2 * r + 1] + 8.f;
+    }
+    if (__any_sync(0xffffffffu, over)) {
+      float f[RG];
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        float mx = x[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fmaxf(m[r], mx);
+        f[r] = m[r] == -INFINITY ? 0.f : exp2f(m[r] - mx);
+        l[r] *= f[r];
+        m[r] = mx;
+      }
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        const uint64_t f2 = f2_pack(f[2 * r], f[2 * r + 1]);
+#pragma unroll
+        for (int k = 0; k < KD; ++k) acc[k][r] = f2_mul(acc[k][r], f2);
+      }
+    }
+    const float sv = ok ? svr : 0.f;
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      const float p = ok ? exp2f(x[r] - m[r]) : 0.f;
+      l[r] += p;
+      x[r] = p * sv;
+    }
+#pragma unroll
+    for (int r = 0; r < RP; ++r) *reinterpret_cast<float2 *>(wts + lane * RG + 2 * r) = make_float2(x[2 * r], x[2 * r + 1]);
+    __syncwarp();
+
+    // ---- values: this lane's dimensions over the block's seen tokens ----
+    for (unsigned left = mask; left; left &= left - 1) {
+      const int j = __ffs(left) - 1;
+      uint64_t w2[RP];
+      if constexpr (RG >= 4) {
+#pragma unroll
+        for (int r = 0; r < RG / 4; ++r) {
+          const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(wts + j * RG + 4 * r);
+          w2[2 * r] = u.x;
+          w2[2 * r + 1] = u.y;
+        }
+      } else {
+        w2[0] = *reinterpret_cast<const uint64_t *>(wts + j * RG);
+      }
+      const uint32_t *vr = reinterpret_cast<const uint32_t *>(vc + j * RS);
+#pragma unroll
+      for (int u = 0; u < KD / 4; ++u) {
+        const uint32_t f = quad_fields<BITS>(vr, (KD / 4) * lane + u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t off = e == 0 ? (f << 3) & 0x78u : (f >> (4 * e - 3)) & 0x78u;
+          const uint64_t c = *reinterpret_cast<const uint64_t *>(tab + off);
+#pragma unroll
+          for (int r = 0; r < RP; ++r) acc[4 * u + e][r] = f2_fma(c, w2[r], acc[4 * u + e][r]);
+        }
+      }
+    }
+    __syncwarp();   // the stage and the weights may be overwritten
+  }
+
+  // ---- merge the four warps in a fixed order, one state per query row ----
+  cp_async_wait<0>();
+#pragma unroll
+  for (int r = 0; r < RG; ++r) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+    if (lane == 0) ml[warp * RG + r] = make_float2(m[r], l[r]);
+  }
+  __syncthreads();   // every warp is done with its stages
+  float *sl = reinterpret_cast<float *>(smem);   // [warp][RG][D]
+#pragma unroll
+  for (int r = 0; r < RP; ++r) {
+#pragma unroll
+    for (int k = 0; k < KD; ++k) {
+      float u0, u1;
+      f2_unpack(acc[k][r], u0, u1);
+      sl[(warp * RG + 2 * r) * D + KD * lane + k] = u0;
+      sl[(warp * RG + 2 * r + 1) * D + KD * lane + k] = u1;
+    }
+  }
+  __syncthreads();
+  for (int h = 0; h < rows; ++h) {
+    float mx = -INFINITY, f[kAnyWarps], lt = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAnyWarps; ++w) mx = fmaxf(mx, ml[w * RG + h].x);
+#pragma unroll
+    for (int w = 0; w < kAnyWarps; ++w) {
+      const float2 u = ml[w * RG + h];
+      f[w] = u.x == -INFINITY ? 0.f : exp2f(u.x - mx);
+      lt += u.y * f[w];
+    }
+    const long long slot = group_slot(a, grp, kvh, h, split);
+    for (int i = tid; i < D; i += kAnyThreads) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAnyWarps; ++w) sum += sl[(w * RG + h) * D + i] * f[w];
+      a.ws_acc[slot * D + i] = sum;
+    }
+    if (tid == 0) a.ws_ml[slot] = make_float2(mx == -INFINITY ? -INFINITY : mx * 0.69314718055994531f, lt);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+template <typename T, int D>
+int launch_prep_rotate(int variant, const SplitArgs &a, cudaStream_t st) {
+  const long long rows = static_cast<long long>(a.batch) * a.hq;
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  if (variant == ISOQ_FULL)
+    prep_rotate_kernel<T, D, true><<<grid, 128, 0, st>>>(a);
+  else
+    prep_rotate_kernel<T, D, false><<<grid, 128, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "query rotation launch: %s", cudaGetErrorString(e));
+}
+
+int run_prep_rotate(int dtype, int d, int variant, const SplitArgs &a, cudaStream_t st) {
+  if (dtype == ISOQ_F16) {
+    if (d == 128) return launch_prep_rotate<__half, 128>(variant, a, st);
+    if (d == 256) return launch_prep_rotate<__half, 256>(variant, a, st);
+    return launch_prep_rotate<__half, 512>(variant, a, st);
+  }
+  if (d == 128) return launch_prep_rotate<float, 128>(variant, a, st);
+  if (d == 256) return launch_prep_rotate<float, 256>(variant, a, st);
+  return launch_prep_rotate<float, 512>(variant, a, st);
+}
+
+template <int D, int BITS, int RG>
+int launch_split_any(const SplitArgs &a, cudaStream_t st) {
+  using C = AnyCfg<D, BITS, RG>;
+  auto kernel = split_any_kernel<D, BITS, RG>;
+  const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (c != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "split: %s", cudaGetErrorString(c));
+  const int nx = a.mode == kSplitPrefix && a.n_splits_p > a.n_splits ? a.n_splits_p : a.n_splits;
+  cudaError_t e = launch_pdl(kernel, dim3(nx, a.hkv, group_count(a, a.mode)), dim3(kAnyThreads), C::SMEM, st, a);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "split launch: %s", cudaGetErrorString(e));
+}
+
+template <int D, int BITS>
+int run_split_any_r(const SplitArgs &a, cudaStream_t st) {
+  const int rows = a.mode == kSplitPrefix && a.zrow_size_p > a.zrow_size ? a.zrow_size_p : a.zrow_size;
+  if (rows <= 2) return launch_split_any<D, BITS, 2>(a, st);
+  if (rows <= 4) return launch_split_any<D, BITS, 4>(a, st);
+  return launch_split_any<D, BITS, 8>(a, st);
+}
+
+template <int D>
+int run_split_any_b(int bits, const SplitArgs &a, cudaStream_t st) {
+  if (bits == 2) return run_split_any_r<D, 2>(a, st);
+  if (bits == 3) return run_split_any_r<D, 3>(a, st);
+  return run_split_any_r<D, 4>(a, st);
+}
+
+int run_split_any(int d, int bits, const SplitArgs &a, cudaStream_t st) {
+  if (d == 128) return run_split_any_b<128>(bits, a, st);
+  if (d == 256) return run_split_any_b<256>(bits, a, st);
+  return run_split_any_b<512>(bits, a, st);
+}

@@ -337,6 +337,146 @@ int isoq_prefill_attention(const void *q_dev, int dtype, const uint8_t *packed_k
                            void *out_dev, isoq_stream_t stream);
 
 /*
+ * Serving attention: the operators below extend the decode and the prefill
+ * to what a server keeps around the packed cache.  The method's pages have no
+ * counterpart to them; they are this library's.
+ *
+ * Sliding window with sink tokens, decode.  As isoq_decode_attention over the
+ * T = min(max(seq_lens[b], 0), Tmax) tokens of a row, of which the query (at
+ * position T - 1) sees those with j >= T - window or j < n_sink; the work
+ * follows window + n_sink, not T.  Tokens that are not seen are not read, or
+ * weigh nothing whatever their codes and norms hold.  A row that sees nothing
+ * gives zeros.
+ *   window, n_sink  >= 0; values above Tmax count as Tmax (no window).
+ *   workspace_dev   at least isoq_decode_window_workspace_size(...) bytes
+ *                   (a function of the same arguments), 256-byte aligned.
+ * The other arguments and rules as isoq_decode_attention; B <= 16384.
+ * Float16 queries with 3-bit codes, d in {128, 256}, Tmax % 8 == 0 and norms
+ * aligned to 16 bytes take the integer tensor-core split, everything else a
+ * float32 one.  isoq_decode_window_workspace_size returns 0 on invalid shapes.
+ */
+size_t isoq_decode_window_workspace_size(int B, int Hq, int Hkv, int64_t Tmax, int d, int64_t window,
+                                         int64_t n_sink);
+int isoq_decode_attention_window(const void *q_dev, int dtype, const uint8_t *packed_k_dev,
+                                 const uint8_t *packed_v_dev, const uint16_t *norms_k_dev,
+                                 const uint16_t *norms_v_dev, const int32_t *seq_lens_dev, int B,
+                                 int Hq, int Hkv, int64_t Tmax, int d, int bits, int variant,
+                                 const float *params_k_dev, const float *params_v_dev, float scale,
+                                 int64_t window, int64_t n_sink, void *out_dev,
+                                 void *workspace_dev, size_t workspace_bytes, isoq_stream_t stream);
+
+/*
+ * The same for chunked prefill: as isoq_prefill_attention (its types, shapes
+ * and rules), each query at position p seeing the tokens j <= p with
+ * j > p - window or j < n_sink.
+ */
+int isoq_prefill_attention_window(const void *q_dev, int dtype, const uint8_t *packed_k_dev,
+                                  const uint8_t *packed_v_dev, const uint16_t *norms_k_dev,
+                                  const uint16_t *norms_v_dev, const int32_t *seq_lens_dev, int B,
+                                  int Tq, int Hq, int Hkv, int64_t Tmax, int d, int bits,
+                                  int variant, const float *params_k_dev,
+                                  const float *params_v_dev, float scale, int64_t window,
+                                  int64_t n_sink, void *out_dev, isoq_stream_t stream);
+
+/*
+ * Decode of a batch whose rows share a prefix.  Row b attends to the first
+ * P = min(max(*prefix_len_dev, 0), prefix_tokens) tokens of one packed prefix
+ * and to its own T_b = min(max(seq_lens[b], 0), Tmax) tokens, under one
+ * softmax; the prefix is unpacked once for all rows of the batch (up to 8
+ * query heads at a time), not once per row.  Both parts use the same rotation
+ * parameters.
+ *   prefix_k_dev, prefix_v_dev  [Hkv] rows of prefix_head_stride packed
+ *                vectors, of which the first prefix_tokens may be read;
+ *                16-byte aligned (a row of a larger cache is a valid prefix).
+ *   prefix_norms_k_dev, prefix_norms_v_dev  the same for the float16 norms.
+ *   prefix_len_dev  one int32 on the device.
+ *   workspace_dev   at least isoq_decode_prefix_workspace_size(...) bytes.
+ * prefix_tokens = 0 is allowed (the prefix pointers may then be NULL).  The
+ * other arguments and rules as isoq_decode_attention; B <= 16384.  The
+ * tensor-core splits need what isoq_decode_attention_window names, for
+ * prefix_head_stride and prefix_tokens too.
+ */
+size_t isoq_decode_prefix_workspace_size(int B, int Hq, int Hkv, int64_t prefix_tokens,
+                                         int64_t Tmax, int d);
+int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *prefix_k_dev,
+                                 const uint8_t *prefix_v_dev, const uint16_t *prefix_norms_k_dev,
+                                 const uint16_t *prefix_norms_v_dev, const int32_t *prefix_len_dev,
+                                 int64_t prefix_tokens, int64_t prefix_head_stride,
+                                 const uint8_t *packed_k_dev, const uint8_t *packed_v_dev,
+                                 const uint16_t *norms_k_dev, const uint16_t *norms_v_dev,
+                                 const int32_t *seq_lens_dev, int B, int Hq, int Hkv, int64_t Tmax,
+                                 int d, int bits, int variant, const float *params_k_dev,
+                                 const float *params_v_dev, float scale, void *out_dev,
+                                 void *workspace_dev, size_t workspace_bytes, isoq_stream_t stream);
+
+/*
+ * Paged cache.  Pages of page_tokens tokens (16, 32, 64, 128 or 256), a pool
+ * per tensor: packed K and V [n_pages][Hkv][page_tokens][d*bits/8] (16-byte
+ * aligned), norms [n_pages][Hkv][page_tokens].  Token t of row b is in page
+ * block_table[b][t / page_tokens], at t mod page_tokens; its slot is
+ * page * page_tokens + t mod page_tokens.
+ *
+ * isoq_build_block_tables: the pages and slots of the tokens that a step adds.
+ * Row b holds seq_lens[b] tokens (values below 0 count as 0) and gets
+ * new_lens[b] more.  The pages it lacks are taken from the free list in row
+ * order: free_pages[h], free_pages[h + 1], ..., with h = *free_head_dev (0 if
+ * that is NULL), and written behind the row's pages in block_table; entries
+ * that belong to no page taken here are left as they are.
+ *   block_table_dev  [B][max_pages] int32, read and written in place.
+ *   slot_map_dev     [n_slots] int64: the slots of all new tokens, row after
+ *                    row, then -1.
+ *   row_start_dev    [B + 1] int32: where a row's new tokens begin in
+ *                    slot_map; the last entry is their number.
+ *   total_lens_dev   [B] int32: seq_lens + new_lens.
+ *   pages_used_dev   one int32: pages taken (what a caller adds to its head).
+ * A row that does not fit (more tokens than the table row or slot_map holds,
+ * new_lens[b] < 0, or a free list that the pages up to its own exhaust) takes
+ * no page: its slots are -1, total_lens[b] is seq_lens[b], and the next
+ * isoq_check_device_error reports ISOQ_ERR_INVALID_ARG.  No output may overlap
+ * an input or another output.  The result does not depend on scheduling.
+ *
+ * isoq_paged_append: Algorithm 1 on N new tokens, written to their slots.
+ *   k_new_dev, v_new_dev  [N][Hkv][d] of `dtype`, 16-byte aligned.
+ *   slot_map_dev  [N] int64; a negative slot's token is skipped, one beyond
+ *                 the pages is skipped and reported by isoq_check_device_error
+ *                 (ISOQ_ERR_INVALID_ARG).  No slot may occur twice.
+ * Codes and norms are the decisions of float64 arithmetic on the float32
+ * parameters (coordinates close to a threshold, and norms close to a float16
+ * rounding boundary, are summed again in double).  N = 0 is a no-op.
+ *
+ * isoq_paged_decode_attention: isoq_decode_attention_window over the pages.
+ *   block_table_dev [B][max_pages]; only entries of pages that hold a token
+ *                 the query sees are used.  One outside [0, n_pages) is
+ *                 reported by isoq_check_device_error (ISOQ_ERR_INVALID_ARG)
+ *                 and the row's output is then undefined; nothing outside the
+ *                 pages is read.
+ *   max_len       a bound on the lengths, at most max_pages * page_tokens;
+ *                 longer rows are cut to it.  The closer it is, the better the
+ *                 splits fill the GPU.
+ *   window, n_sink  as isoq_decode_attention_window (window >= max_len: none).
+ *   workspace_dev at least isoq_decode_window_workspace_size(B, Hq, Hkv,
+ *                 max_len, d, window, n_sink) bytes.
+ */
+int isoq_build_block_tables(const int32_t *seq_lens_dev, const int32_t *new_lens_dev,
+                            const int32_t *free_pages_dev, const int32_t *free_head_dev, int n_free,
+                            int B, int page_tokens, int max_pages, int32_t *block_table_dev,
+                            int64_t n_slots, int64_t *slot_map_dev, int32_t *row_start_dev,
+                            int32_t *total_lens_dev, int32_t *pages_used_dev, isoq_stream_t stream);
+int isoq_paged_append(const void *k_new_dev, const void *v_new_dev, int dtype, uint8_t *pages_k_dev,
+                      uint8_t *pages_v_dev, uint16_t *norms_k_dev, uint16_t *norms_v_dev,
+                      const int64_t *slot_map_dev, int64_t N, int Hkv, int n_pages, int page_tokens,
+                      int d, int bits, int variant, const float *params_k_dev,
+                      const float *params_v_dev, isoq_stream_t stream);
+int isoq_paged_decode_attention(const void *q_dev, int dtype, const uint8_t *pages_k_dev,
+                                const uint8_t *pages_v_dev, const uint16_t *norms_k_dev,
+                                const uint16_t *norms_v_dev, const int32_t *block_table_dev,
+                                const int32_t *seq_lens_dev, int B, int Hq, int Hkv, int n_pages,
+                                int page_tokens, int max_pages, int64_t max_len, int d, int bits,
+                                int variant, const float *params_k_dev, const float *params_v_dev,
+                                float scale, int64_t window, int64_t n_sink, void *out_dev,
+                                void *workspace_dev, size_t workspace_bytes, isoq_stream_t stream);
+
+/*
  * RotorQuant comparator (the RotorQuant page; [IQ] abstract compares
  * IsoQuant's kernels with it on the stage-1 path).  Each vector is padded
  * to 3G dimensions, G = ceil(d / 3), each group of three is rotated by its
@@ -374,7 +514,8 @@ int isoq_rotor_dequantize(const uint8_t *codes_dev, const uint16_t *norms_dev, i
  * `stream`.  Returns ISOQ_OK, ISOQ_ERR_TIMEOUT if a kernel's bounded wait
  * gave up since the last check (the kernel then stopped early and its
  * outputs are incomplete), ISOQ_ERR_INVALID_ARG if a decode append met a
- * row that already held Tmax tokens, or ISOQ_ERR_CUDA (among others when
+ * row that already held Tmax tokens, a page index or slot was outside the
+ * pages, or block tables had no room for a request, or ISOQ_ERR_CUDA (among others when
  * the prefill kernel found its dynamic shared memory off a 1024-byte
  * boundary and returned without output).
  */
