@@ -10,6 +10,7 @@ library raises at import of this module's functions.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -171,9 +172,15 @@ def isoq_decode_workspace_size(B: int, Hq: int, Hkv: int, Tmax: int, d: int) -> 
 # Device entry points (torch tensors)
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -507,65 +514,71 @@ def isoq_decode_static_workspace_bytes() -> int:
 
 # ---------------------------------------------------------------------------
 # Serving attention: window and sinks, shared prefix, pages
+#
+# A decode step makes these calls once per layer, and a small one takes about
+# 10 us on the GPU: the checks are one expression over plain attributes, and
+# only where it fails does _why look for the argument that does not fit.
 # ---------------------------------------------------------------------------
 
-def _scale(scale: Optional[float], d: int) -> float:
-    return 1.0 / math.sqrt(d) if scale is None else float(scale)
-
-
-def _contiguous(**tensors):
-    for name, t in tensors.items():
+def _refuse(dtypes, contiguous, conditions, tensors):
+    """Raises for the first argument that does not fit."""
+    for name, t, dtype in dtypes:
+        if t is not None and t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    for name, t in contiguous:
         if t is not None and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    for ok, what in conditions:
+        if not ok:
+            raise ValueError(what)
+    _require_cuda(*tensors)
+    raise ValueError("the arguments do not fit together")
 
 
-def _typed(dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+def _cache_refusal(q, pk, pv, nk, nv, lens, prk, prv, hkv, d, bits, batch, more, tensors):
+    """_refuse for a call with a packed cache [a][b][c][d*bits/8], its norms
+    and rotations; `more`: further (condition, what) pairs."""
+    t = _torch()
+    _refuse([("packed K", pk, t.uint8), ("packed V", pv, t.uint8), ("the norms of K", nk, t.float16),
+             ("the norms of V", nv, t.float16), ("seq_lens", lens, t.int32), ("params_k", prk, t.float32),
+             ("params_v", prv, t.float32)],
+            [("q", q), ("packed K", pk), ("packed V", pv), ("the norms of K", nk), ("the norms of V", nv),
+             ("seq_lens", lens), ("params_k", prk), ("params_v", prv)],
+            [(pk.shape == pv.shape and nk.shape == nv.shape and pk.shape[:-1] == nk.shape,
+              "packed K, packed V and their norms do not have one shape"),
+             (pk.shape[-1] == isoq_packed_bytes(d, bits), "packed row size does not match d and bits"),
+             (lens is None or lens.numel() == batch, f"seq_lens does not have {batch} entries"),
+             (prk.numel() == prv.numel() == hkv * 2 * d, "rotation parameters are not [Hkv][d/4][8]"), *more], tensors)
 
 
-def _check_cache(packed_k, packed_v, norms_k, norms_v, d, bits):
-    """Shapes and types of a packed cache [a][b][c][d*bits/8] with its norms
-    [a][b][c]; returns its shape."""
-    torch = _torch()
-    _typed(torch.uint8, packed_k=packed_k, packed_v=packed_v)
-    _typed(torch.float16, norms_k=norms_k, norms_v=norms_v)
-    if packed_k.shape != packed_v.shape or packed_k.shape[:-1] != norms_k.shape or norms_k.shape != norms_v.shape:
-        raise ValueError("packed K, packed V and their norms do not have one shape")
-    if packed_k.shape[-1] != isoq_packed_bytes(d, bits):
-        raise ValueError("packed row size does not match d and bits")
-    return packed_k.shape
+def _fits(q, pk, pv, nk, nv, lens, prk, prv, hkv, d, bits, batch) -> bool:
+    """Types, shapes and layout of a packed cache and what goes with it."""
+    t = _torch()
+    n = hkv * 2 * d
+    return (pk.dtype is pv.dtype is t.uint8 and nk.dtype is nv.dtype is t.float16 and lens.dtype is t.int32 and
+            prk.dtype is prv.dtype is t.float32 and pk.shape == pv.shape and nk.shape == nv.shape and
+            pk.shape[:-1] == nk.shape and pk.shape[-1] * 8 == d * bits and lens.numel() == batch and
+            prk.numel() == n and prv.numel() == n and q.is_contiguous() and pk.is_contiguous() and
+            pv.is_contiguous() and nk.is_contiguous() and nv.is_contiguous() and lens.is_contiguous() and
+            prk.is_contiguous() and prv.is_contiguous())
 
 
-def _check_params(params_k, params_v, hkv, d):
-    torch = _torch()
-    _typed(torch.float32, params_k=params_k, params_v=params_v)
-    _contiguous(params_k=params_k, params_v=params_v)
-    for p in (params_k, params_v):
-        if p.numel() != hkv * 2 * d:
-            raise ValueError("rotation parameters are not [Hkv][d/4][8]")
-
-
-def _check_lens(lens, n, name):
-    torch = _torch()
-    _typed(torch.int32, **{name: lens})
-    _contiguous(**{name: lens})
-    if lens.numel() != n:
-        raise ValueError(f"{name} does not have {n} entries")
-
-
-def _check_out(out, like):
-    if out.shape != like.shape or out.dtype != like.dtype or not out.is_contiguous():
+def _out_of(out, q):
+    if out is None:
+        return _torch().empty_like(q)
+    if out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, with the shape and dtype of q")
+    if out.device != q.device:
+        raise ValueError("all tensors must be on the same device")
+    return out
 
 
 class _on:
     """The device made current for a launch, where it is not already."""
 
-    def __init__(self, dev):
-        torch = _torch()
-        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    def __init__(self, index):
+        cuda = _torch().cuda
+        self.guard = None if cuda.current_device() == index else cuda.device(index)
 
     def __enter__(self):
         if self.guard is not None:
@@ -576,18 +589,32 @@ class _on:
             self.guard.__exit__(*exc)
 
 
+def _raw_stream(index: int, stream) -> int:
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _scratch(workspace, nbytes, dev):
     """The caller's workspace, or one from torch's allocator; and its bytes."""
     if workspace is None:
-        return _torch().empty(nbytes, dtype=_torch().uint8, device=dev), nbytes
-    _contiguous(workspace=workspace)
+        t = _torch()
+        return t.empty(nbytes, dtype=t.uint8, device=dev), nbytes
+    if not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be contiguous and on the device of q")
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _scale(scale: Optional[float], d: int) -> float:
+    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+
+@functools.lru_cache(maxsize=256)
 def isoq_decode_window_workspace_size(B: int, Hq: int, Hkv: int, Tmax: int, d: int, window: int, n_sink: int) -> int:
     return lib().isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink)
 
 
+@functools.lru_cache(maxsize=256)
 def isoq_decode_prefix_workspace_size(B: int, Hq: int, Hkv: int, prefix_tokens: int, Tmax: int, d: int) -> int:
     return lib().isoq_decode_prefix_workspace_size(B, Hq, Hkv, prefix_tokens, Tmax, d)
 
@@ -597,24 +624,26 @@ def isoq_decode_attention_window(q, packed_k, packed_v, norms_k, norms_v, seq_le
                                  out=None, workspace=None, stream=None):
     """Decode attention of q [B][Hq][d] over packed K/V, of which a row sees
     its last ``window`` tokens and its first ``n_sink``; returns out (as q)."""
-    torch = _torch()
     B, Hq, d = q.shape
-    b, Hkv, Tmax, _ = _check_cache(packed_k, packed_v, norms_k, norms_v, d, bits)
-    _contiguous(q=q, packed_k=packed_k, packed_v=packed_v, norms_k=norms_k, norms_v=norms_v)
-    if b != B:
-        raise ValueError("q and the cache differ in their batch")
-    _check_lens(seq_lens, B, "seq_lens")
-    _check_params(params_k, params_v, Hkv, d)
-    dev = _require_cuda(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, out, workspace)
-    out = torch.empty_like(q) if out is None else out
-    _check_out(out, q)
-    with _on(dev):
-        workspace, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink), dev)
+    batch, Hkv, Tmax, _ = packed_k.shape
+    index = q.get_device()
+    if not (batch == B and _fits(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B)
+            and packed_k.get_device() == packed_v.get_device() == norms_k.get_device() == norms_v.get_device() ==
+            seq_lens.get_device() == params_k.get_device() == params_v.get_device() == index >= 0):
+        _cache_refusal(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B,
+                       [(batch == B, "q and the cache differ in their batch")],
+                       (q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v))
+    with _on(index):
+        out = _out_of(out, q)
+        workspace, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink),
+                                 q.device)
         st = lib().isoq_decode_attention_window(
-            _ptr(q), _dtype_code(q), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v), _ptr(seq_lens), B, Hq,
-            Hkv, Tmax, d, bits, variant, _ptr(params_k), _ptr(params_v), _scale(scale, d), window, n_sink, _ptr(out),
-            _ptr(workspace), ws, _stream(dev, stream))
-    _check(st, "isoq_decode_attention_window")
+            q.data_ptr(), _dtype_code(q), packed_k.data_ptr(), packed_v.data_ptr(), norms_k.data_ptr(),
+            norms_v.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, Tmax, d, bits, variant, params_k.data_ptr(),
+            params_v.data_ptr(), _scale(scale, d), window, n_sink, out.data_ptr(), workspace.data_ptr(), ws,
+            _raw_stream(index, stream))
+    if st:
+        _check(st, "isoq_decode_attention_window")
     return out
 
 
@@ -624,23 +653,23 @@ def isoq_prefill_attention_window(q, packed_k, packed_v, norms_k, norms_v, seq_l
     """Causal attention of q [B][Tq][Hq][d] over the packed cache that holds
     the chunk, each query seeing the last ``window`` tokens up to its own and
     the first ``n_sink``; returns out (as q)."""
-    torch = _torch()
     B, Tq, Hq, d = q.shape
-    b, Hkv, Tmax, _ = _check_cache(packed_k, packed_v, norms_k, norms_v, d, bits)
-    _contiguous(q=q, packed_k=packed_k, packed_v=packed_v, norms_k=norms_k, norms_v=norms_v)
-    if b != B:
-        raise ValueError("q and the cache differ in their batch")
-    _check_lens(seq_lens, B, "seq_lens")
-    _check_params(params_k, params_v, Hkv, d)
-    dev = _require_cuda(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, out)
-    out = torch.empty_like(q) if out is None else out
-    _check_out(out, q)
-    with _on(dev):
+    batch, Hkv, Tmax, _ = packed_k.shape
+    index = q.get_device()
+    if not (batch == B and _fits(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B)
+            and packed_k.get_device() == packed_v.get_device() == norms_k.get_device() == norms_v.get_device() ==
+            seq_lens.get_device() == params_k.get_device() == params_v.get_device() == index >= 0):
+        _cache_refusal(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B,
+                       [(batch == B, "q and the cache differ in their batch")],
+                       (q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v))
+    with _on(index):
+        out = _out_of(out, q)
         st = lib().isoq_prefill_attention_window(
-            _ptr(q), _dtype_code(q), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v), _ptr(seq_lens), B, Tq,
-            Hq, Hkv, Tmax, d, bits, variant, _ptr(params_k), _ptr(params_v), _scale(scale, d), window, n_sink, _ptr(out),
-            _stream(dev, stream))
-    _check(st, "isoq_prefill_attention_window")
+            q.data_ptr(), _dtype_code(q), packed_k.data_ptr(), packed_v.data_ptr(), norms_k.data_ptr(),
+            norms_v.data_ptr(), seq_lens.data_ptr(), B, Tq, Hq, Hkv, Tmax, d, bits, variant, params_k.data_ptr(),
+            params_v.data_ptr(), _scale(scale, d), window, n_sink, out.data_ptr(), _raw_stream(index, stream))
+    if st:
+        _check(st, "isoq_prefill_attention_window")
     return out
 
 
@@ -651,35 +680,45 @@ def isoq_decode_attention_prefix(q, prefix_k, prefix_v, prefix_norms_k, prefix_n
     all rows share (its first ``prefix_len`` tokens, one int32 on the device)
     and each row's own packed K/V; returns out (as q).  The prefix may be one
     row of a larger cache: its KV heads may lie apart."""
-    torch = _torch()
+    t = _torch()
     B, Hq, d = q.shape
-    b, Hkv, Tmax, pb = _check_cache(packed_k, packed_v, norms_k, norms_v, d, bits)
-    _contiguous(q=q, packed_k=packed_k, packed_v=packed_v, norms_k=norms_k, norms_v=norms_v)
-    if b != B:
-        raise ValueError("q and the cache differ in their batch")
-    heads, Tp, _ = _check_cache(prefix_k, prefix_v, prefix_norms_k, prefix_norms_v, d, bits)
-    if heads != Hkv:
-        raise ValueError("the prefix and the cache differ in their KV heads")
+    batch, Hkv, Tmax, pb = packed_k.shape
+    heads, Tp, _ = prefix_k.shape
+    index = q.get_device()
     apart = prefix_norms_k.stride(0) if Hkv > 1 else Tp
-    for t, row in ((prefix_k, pb), (prefix_v, pb), (prefix_norms_k, 1), (prefix_norms_v, 1)):
-        if Tp > 0 and ((Hkv > 1 and t.stride(0) != apart * row) or (Tp > 1 and t.stride(1) != row) or
-                       (t.dim() == 3 and t.stride(2) != 1)):
-            raise ValueError("the prefix's tokens must be contiguous, its KV heads equally far apart in all tensors")
-    _check_lens(seq_lens, B, "seq_lens")
-    _check_lens(prefix_len, 1, "prefix_len")
-    _check_params(params_k, params_v, Hkv, d)
-    dev = _require_cuda(q, prefix_k, prefix_v, prefix_norms_k, prefix_norms_v, prefix_len, packed_k, packed_v, norms_k,
-                        norms_v, seq_lens, params_k, params_v, out, workspace)
-    out = torch.empty_like(q) if out is None else out
-    _check_out(out, q)
-    with _on(dev):
-        workspace, ws = _scratch(workspace, isoq_decode_prefix_workspace_size(B, Hq, Hkv, Tp, Tmax, d), dev)
+
+    def laid_out(x, width):   # tokens contiguous, KV heads `apart` tokens apart
+        return Tp == 0 or ((Hkv == 1 or x.stride(0) == apart * width) and (Tp == 1 or x.stride(1) == width) and
+                           (x.dim() == 2 or x.stride(2) == 1))
+
+    prefix_fits = (prefix_k.dtype is prefix_v.dtype is t.uint8 and prefix_norms_k.dtype is prefix_norms_v.dtype is t.float16 and
+                   prefix_k.shape == prefix_v.shape and prefix_norms_k.shape == prefix_norms_v.shape == prefix_k.shape[:-1]
+                   and heads == Hkv and prefix_k.shape[-1] == pb and apart >= Tp and laid_out(prefix_k, pb) and
+                   laid_out(prefix_v, pb) and laid_out(prefix_norms_k, 1) and laid_out(prefix_norms_v, 1))
+    if not (batch == B and prefix_fits and prefix_len.dtype is t.int32 and prefix_len.numel() == 1 and
+            _fits(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B) and
+            packed_k.get_device() == packed_v.get_device() == norms_k.get_device() == norms_v.get_device() ==
+            seq_lens.get_device() == params_k.get_device() == params_v.get_device() == prefix_k.get_device() ==
+            prefix_v.get_device() == prefix_norms_k.get_device() == prefix_norms_v.get_device() ==
+            prefix_len.get_device() == index >= 0):
+        _cache_refusal(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B,
+                       [(batch == B, "q and the cache differ in their batch"),
+                        (prefix_fits, "the prefix is not [Hkv][Tp] packed rows and norms of the cache's kind, its tokens "
+                                      "contiguous and its KV heads equally far apart in all four tensors"),
+                        (prefix_len.dtype is t.int32 and prefix_len.numel() == 1, "prefix_len is one int32")],
+                       (q, prefix_k, prefix_v, prefix_norms_k, prefix_norms_v, prefix_len, packed_k, packed_v, norms_k,
+                        norms_v, seq_lens, params_k, params_v))
+    with _on(index):
+        out = _out_of(out, q)
+        workspace, ws = _scratch(workspace, isoq_decode_prefix_workspace_size(B, Hq, Hkv, Tp, Tmax, d), q.device)
         st = lib().isoq_decode_attention_prefix(
-            _ptr(q), _dtype_code(q), _ptr(prefix_k), _ptr(prefix_v), _ptr(prefix_norms_k), _ptr(prefix_norms_v),
-            _ptr(prefix_len), Tp, max(apart, Tp), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v),
-            _ptr(seq_lens), B, Hq, Hkv, Tmax, d, bits, variant, _ptr(params_k), _ptr(params_v), _scale(scale, d),
-            _ptr(out), _ptr(workspace), ws, _stream(dev, stream))
-    _check(st, "isoq_decode_attention_prefix")
+            q.data_ptr(), _dtype_code(q), prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_norms_k.data_ptr(),
+            prefix_norms_v.data_ptr(), prefix_len.data_ptr(), Tp, apart, packed_k.data_ptr(), packed_v.data_ptr(),
+            norms_k.data_ptr(), norms_v.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, Tmax, d, bits, variant,
+            params_k.data_ptr(), params_v.data_ptr(), _scale(scale, d), out.data_ptr(), workspace.data_ptr(), ws,
+            _raw_stream(index, stream))
+    if st:
+        _check(st, "isoq_decode_attention_prefix")
     return out
 
 
@@ -689,39 +728,50 @@ def isoq_build_block_tables(seq_lens, new_lens, free_pages, block_table, page_to
     the pages that the rows lack from ``free_pages`` (from ``free_head`` on) into
     ``block_table`` [B][max_pages], in place; returns (slot_map [n_slots],
     row_start [B + 1], total_lens [B], pages_used [1])."""
-    torch = _torch()
+    t = _torch()
     B, max_pages = block_table.shape
-    _check_lens(seq_lens, B, "seq_lens")
-    _check_lens(new_lens, B, "new_lens")
-    _typed(torch.int32, free_pages=free_pages, block_table=block_table, free_head=free_head, row_start=row_start,
-           total_lens=total_lens, pages_used=pages_used)
-    _typed(torch.int64, slot_map=slot_map)
-    _contiguous(free_pages=free_pages, block_table=block_table, slot_map=slot_map, row_start=row_start,
-                total_lens=total_lens, pages_used=pages_used)
-    if slot_map is None and n_slots is None:
-        raise ValueError("n_slots (or slot_map) says how many new tokens there may be")
-    dev = _require_cuda(seq_lens, new_lens, free_pages, block_table, free_head, slot_map, row_start, total_lens, pages_used)
+    index = block_table.get_device()
     if slot_map is None:
-        slot_map = torch.empty(n_slots, dtype=torch.int64, device=dev)
-    elif n_slots is not None and slot_map.numel() != n_slots:
-        raise ValueError("slot_map does not have n_slots entries")
-    if row_start is None:
-        row_start = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    if total_lens is None:
-        total_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    if pages_used is None:
-        pages_used = torch.empty(1, dtype=torch.int32, device=dev)
-    for name, t, n in (("row_start", row_start, B + 1), ("total_lens", total_lens, B), ("pages_used", pages_used, 1)):
-        if t.numel() != n:
-            raise ValueError(f"{name} does not have {n} entries")
-    if free_head is not None and free_head.numel() != 1:
-        raise ValueError("free_head is one int32")
-    with _on(dev):
+        if n_slots is None:
+            raise ValueError("n_slots (or slot_map) says how many new tokens there may be")
+        slots = n_slots
+    else:
+        slots = slot_map.numel()
+    ints = (seq_lens, new_lens, free_pages, block_table)
+    given = [x for x in (free_head, row_start, total_lens, pages_used) if x is not None]
+    if not (all(x.dtype is t.int32 and x.is_contiguous() and x.get_device() == index for x in (*ints, *given)) and
+            index >= 0 and seq_lens.numel() == B and new_lens.numel() == B and
+            (free_head is None or free_head.numel() == 1) and (row_start is None or row_start.numel() == B + 1) and
+            (total_lens is None or total_lens.numel() == B) and (pages_used is None or pages_used.numel() == 1) and
+            (slot_map is None or (slot_map.dtype is t.int64 and slot_map.is_contiguous() and
+                                  slot_map.get_device() == index and n_slots in (None, slots)))):
+        names = ("seq_lens", "new_lens", "free_pages", "block_table", "free_head", "row_start", "total_lens", "pages_used")
+        every = (*ints, free_head, row_start, total_lens, pages_used)
+        _refuse([*((n, x, t.int32) for n, x in zip(names, every)), ("slot_map", slot_map, t.int64)],
+                [*zip(names, every), ("slot_map", slot_map)],
+                [(seq_lens.numel() == B, f"seq_lens does not have {B} entries"),
+                 (new_lens.numel() == B, f"new_lens does not have {B} entries"),
+                 (free_head is None or free_head.numel() == 1, "free_head is one int32"),
+                 (row_start is None or row_start.numel() == B + 1, f"row_start does not have {B + 1} entries"),
+                 (total_lens is None or total_lens.numel() == B, f"total_lens does not have {B} entries"),
+                 (pages_used is None or pages_used.numel() == 1, "pages_used is one int32"),
+                 (n_slots in (None, slots), "slot_map does not have n_slots entries")], (*every, slot_map))
+    with _on(index):
+        dev = block_table.device
+        if slot_map is None:
+            slot_map = t.empty(slots, dtype=t.int64, device=dev)
+        if row_start is None:
+            row_start = t.empty(B + 1, dtype=t.int32, device=dev)
+        if total_lens is None:
+            total_lens = t.empty(B, dtype=t.int32, device=dev)
+        if pages_used is None:
+            pages_used = t.empty(1, dtype=t.int32, device=dev)
         st = lib().isoq_build_block_tables(
-            _ptr(seq_lens), _ptr(new_lens), _ptr(free_pages), _ptr(free_head), free_pages.numel(), B, page_tokens,
-            max_pages, _ptr(block_table), slot_map.numel(), _ptr(slot_map), _ptr(row_start), _ptr(total_lens),
-            _ptr(pages_used), _stream(dev, stream))
-    _check(st, "isoq_build_block_tables")
+            seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), _ptr(free_head), free_pages.numel(), B,
+            page_tokens, max_pages, block_table.data_ptr(), slots, slot_map.data_ptr(), row_start.data_ptr(),
+            total_lens.data_ptr(), pages_used.data_ptr(), _raw_stream(index, stream))
+    if st:
+        _check(st, "isoq_build_block_tables")
     return slot_map, row_start, total_lens, pages_used
 
 
@@ -731,23 +781,35 @@ def isoq_paged_append(k_new, v_new, pages_k, pages_v, norms_k, norms_v, slot_map
     the pages [n_pages][Hkv][page_tokens][d*bits/8], in place; a negative slot's
     token is skipped.  ``slot_map`` may be longer than N (a slot map of a fixed
     shape): its first N entries count."""
-    torch = _torch()
+    t = _torch()
     N, Hkv, d = k_new.shape
-    n_pages, heads, P, _ = _check_cache(pages_k, pages_v, norms_k, norms_v, d, bits)
-    if heads != Hkv or v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
-        raise ValueError("the new K and V and the pages do not belong together")
-    _typed(torch.int64, slot_map=slot_map)
-    _contiguous(k_new=k_new, v_new=v_new, pages_k=pages_k, pages_v=pages_v, norms_k=norms_k, norms_v=norms_v,
-                slot_map=slot_map)
-    if slot_map.numel() < N:
-        raise ValueError("slot_map has fewer entries than there are new tokens")
-    _check_params(params_k, params_v, Hkv, d)
-    dev = _require_cuda(k_new, v_new, pages_k, pages_v, norms_k, norms_v, slot_map, params_k, params_v)
-    with _on(dev):
+    n_pages, heads, P, _ = pages_k.shape
+    index = k_new.get_device()
+    same = heads == Hkv and v_new.shape == k_new.shape and v_new.dtype is k_new.dtype
+    n = 2 * Hkv * d
+    if not (same and pages_k.dtype is pages_v.dtype is t.uint8 and norms_k.dtype is norms_v.dtype is t.float16 and
+            slot_map.dtype is t.int64 and params_k.dtype is params_v.dtype is t.float32 and
+            pages_k.shape == pages_v.shape and norms_k.shape == norms_v.shape == pages_k.shape[:-1] and
+            pages_k.shape[-1] * 8 == d * bits and slot_map.numel() >= N and params_k.numel() == n and
+            params_v.numel() == n and k_new.is_contiguous() and v_new.is_contiguous() and pages_k.is_contiguous() and
+            pages_v.is_contiguous() and norms_k.is_contiguous() and norms_v.is_contiguous() and
+            slot_map.is_contiguous() and params_k.is_contiguous() and params_v.is_contiguous() and
+            v_new.get_device() == pages_k.get_device() == pages_v.get_device() == norms_k.get_device() ==
+            norms_v.get_device() == slot_map.get_device() == params_k.get_device() == params_v.get_device() == index >= 0):
+        if slot_map.dtype is not t.int64:
+            raise TypeError(f"slot_map must be {t.int64}, not {slot_map.dtype}")
+        _cache_refusal(k_new, pages_k, pages_v, norms_k, norms_v, None, params_k, params_v, Hkv, d, bits, 0,
+                       [(same, "the new K and V and the pages do not belong together"),
+                        (v_new.is_contiguous() and slot_map.is_contiguous(), "v_new and slot_map must be contiguous"),
+                        (slot_map.numel() >= N, "slot_map has fewer entries than there are new tokens")],
+                       (k_new, v_new, pages_k, pages_v, norms_k, norms_v, slot_map, params_k, params_v))
+    with _on(index):
         st = lib().isoq_paged_append(
-            _ptr(k_new), _ptr(v_new), _dtype_code(k_new), _ptr(pages_k), _ptr(pages_v), _ptr(norms_k), _ptr(norms_v),
-            _ptr(slot_map), N, Hkv, n_pages, P, d, bits, variant, _ptr(params_k), _ptr(params_v), _stream(dev, stream))
-    _check(st, "isoq_paged_append")
+            k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), pages_k.data_ptr(), pages_v.data_ptr(),
+            norms_k.data_ptr(), norms_v.data_ptr(), slot_map.data_ptr(), N, Hkv, n_pages, P, d, bits, variant,
+            params_k.data_ptr(), params_v.data_ptr(), _raw_stream(index, stream))
+    if st:
+        _check(st, "isoq_paged_append")
 
 
 def isoq_paged_decode_attention(q, pages_k, pages_v, norms_k, norms_v, block_table, seq_lens, params_k, params_v,
@@ -757,26 +819,33 @@ def isoq_paged_decode_attention(q, pages_k, pages_v, norms_k, norms_v, block_tab
     [B][max_pages] lists; ``max_len`` bounds the lengths (default: what the
     table holds), ``window`` and ``n_sink`` as isoq_decode_attention_window
     (default: all tokens).  Returns out (as q)."""
-    torch = _torch()
+    t = _torch()
     B, Hq, d = q.shape
-    n_pages, Hkv, P, _ = _check_cache(pages_k, pages_v, norms_k, norms_v, d, bits)
-    _typed(torch.int32, block_table=block_table)
-    _contiguous(q=q, pages_k=pages_k, pages_v=pages_v, norms_k=norms_k, norms_v=norms_v, block_table=block_table)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table is not [B][max_pages]")
-    max_pages = block_table.shape[1]
-    max_len = max_pages * P if max_len is None else max_len
-    window = max_len if window is None else window
-    _check_lens(seq_lens, B, "seq_lens")
-    _check_params(params_k, params_v, Hkv, d)
-    dev = _require_cuda(q, pages_k, pages_v, norms_k, norms_v, block_table, seq_lens, params_k, params_v, out, workspace)
-    out = torch.empty_like(q) if out is None else out
-    _check_out(out, q)
-    with _on(dev):
-        workspace, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, max_len, d, window, n_sink), dev)
+    n_pages, Hkv, P, _ = pages_k.shape
+    batch, max_pages = block_table.shape
+    index = q.get_device()
+    if not (batch == B and block_table.dtype is t.int32 and block_table.is_contiguous() and
+            _fits(q, pages_k, pages_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B) and
+            pages_k.get_device() == pages_v.get_device() == norms_k.get_device() == norms_v.get_device() ==
+            block_table.get_device() == seq_lens.get_device() == params_k.get_device() == params_v.get_device() ==
+            index >= 0):
+        _cache_refusal(q, pages_k, pages_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B,
+                       [(batch == B, "block_table is not [B][max_pages]"),
+                        (block_table.dtype is t.int32 and block_table.is_contiguous(), "block_table must be contiguous int32")],
+                       (q, pages_k, pages_v, norms_k, norms_v, block_table, seq_lens, params_k, params_v))
+    if max_len is None:
+        max_len = max_pages * P
+    if window is None:
+        window = max_len
+    with _on(index):
+        out = _out_of(out, q)
+        workspace, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, max_len, d, window, n_sink),
+                                 q.device)
         st = lib().isoq_paged_decode_attention(
-            _ptr(q), _dtype_code(q), _ptr(pages_k), _ptr(pages_v), _ptr(norms_k), _ptr(norms_v), _ptr(block_table),
-            _ptr(seq_lens), B, Hq, Hkv, n_pages, P, max_pages, max_len, d, bits, variant, _ptr(params_k), _ptr(params_v),
-            _scale(scale, d), window, n_sink, _ptr(out), _ptr(workspace), ws, _stream(dev, stream))
-    _check(st, "isoq_paged_decode_attention")
+            q.data_ptr(), _dtype_code(q), pages_k.data_ptr(), pages_v.data_ptr(), norms_k.data_ptr(), norms_v.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, n_pages, P, max_pages, max_len, d, bits, variant,
+            params_k.data_ptr(), params_v.data_ptr(), _scale(scale, d), window, n_sink, out.data_ptr(),
+            workspace.data_ptr(), ws, _raw_stream(index, stream))
+    if st:
+        _check(st, "isoq_paged_decode_attention")
     return out

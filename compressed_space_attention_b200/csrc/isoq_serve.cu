@@ -468,7 +468,7 @@ int isoq_paged_append(const void *k_new_dev, const void *v_new_dev, int dtype, u
     return set_error(ISOQ_ERR_UNSUPPORTED, "page_tokens=%d (16, 32, 64, 128 or 256)", page_tokens);
   if (N < 0 || Hkv <= 0 || n_pages <= 0)
     return set_error(ISOQ_ERR_INVALID_ARG, "Hkv and n_pages must be positive, N >= 0");
-  if (Hkv > 65535 || N >= (1ll << 31) || N * Hkv >= (1ll << 32)) return set_error(ISOQ_ERR_INVALID_ARG, "shape too large");
+  if (Hkv > 32767 || N >= (1ll << 31)) return set_error(ISOQ_ERR_INVALID_ARG, "shape too large");
   if (N == 0) return ISOQ_OK;
   if (!k_new_dev || !v_new_dev || !pages_k_dev || !pages_v_dev || !norms_k_dev || !norms_v_dev || !slot_map_dev ||
       !params_k_dev || !params_v_dev)
@@ -487,7 +487,7 @@ int isoq_paged_append(const void *k_new_dev, const void *v_new_dev, int dtype, u
   a.slot_map = reinterpret_cast<const long long *>(slot_map_dev);
   a.params_k = params_k_dev;
   a.params_v = params_v_dev;
-  a.n_vec = N * Hkv;
+  a.n_tok = N;
   a.n_rows = static_cast<long long>(n_pages) << shift;
   a.hkv = Hkv;
   a.page_shift = shift;

@@ -187,9 +187,14 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
 // Append into page slots
 // ---------------------------------------------------------------------------
 // Algorithm 1 of the compressor on the new tokens' K and V vectors, written
-// to the slots of the slot map.  One warp per vector, lane j holding dims
-// E j .. E j + E - 1 (E = d / 32): float32 norm by shuffles, Walsh-Hadamard
-// stages in the lane and by shuffles, block maps, codes #{k : y > s t_k}.
+// to the slots of the slot map.  d / 16 lanes hold a vector, 16 consecutive
+// dims each (4, 2 or 1 vectors per warp at d = 128, 256, 512): float32 norm,
+// Walsh-Hadamard stages 1 .. 8 in the lane and the others by shuffles, the
+// lane's four block maps with their quaternions kept in registers over the
+// warp's tokens, codes #{k : y > s t_k} by bisection of the positive
+// thresholds, and the packed words from at most one exchange between
+// neighbour lanes.  A warp keeps one (KV head, K or V) and walks its tokens,
+// the next one's loads under way while it works.
 //
 // The codes and norms are the float64 decisions: float32 leaves y within
 // kExactBand s of its value (each of the log2 d stages and of the two
@@ -197,7 +202,8 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
 // most s, in the l2 sense: below 50 2^-24 s = 3e-6 s in all), so a
 // coordinate farther than that from every threshold is decided, and the rest
 // (about 2 vectors in 100 at d = 128 and 3 bits) are summed again in double
-// by the whole warp.  The same for a norm near a float16 rounding boundary.
+// by the vector's lanes.  The same for a norm near a float16 rounding
+// boundary.
 constexpr float kExactBand = 4e-6f;
 
 struct PagedAppendArgs {
@@ -206,215 +212,250 @@ struct PagedAppendArgs {
   uint16_t *norms_k, *norms_v;
   const long long *slot_map;
   const float *params_k, *params_v;
-  long long n_vec, n_rows;     // N Hkv; n_pages P
+  long long n_tok, n_rows;     // N; n_pages P
   int hkv, page_shift;
   float thr[8];                // the positive thresholds, ascending, from 0
   double thr64[15];
 };
 
-// E consecutive elements (8 to 64 bytes, aligned to their size or 16 bytes).
-template <typename T, int E>
-__device__ __forceinline__ void load_elements(const T *src, float (&x)[E]) {
-  if constexpr (sizeof(T) == 4) {
+// Sixteen consecutive elements as loaded, and as float32.
+template <typename T>
+struct Raw16 {
+  uint4 u[sizeof(T)];
+  __device__ __forceinline__ void load(const T *src) {
 #pragma unroll
-    for (int e = 0; e < E; e += 4) {
-      const float4 u = *reinterpret_cast<const float4 *>(src + e);
-      x[e] = u.x;
-      x[e + 1] = u.y;
-      x[e + 2] = u.z;
-      x[e + 3] = u.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; e += 4) {
-      const uint2 u = *reinterpret_cast<const uint2 *>(src + e);
-      const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-      const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-      x[e] = p.x;
-      x[e + 1] = p.y;
-      x[e + 2] = q.x;
-      x[e + 3] = q.y;
-    }
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) u[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
   }
-}
+  __device__ __forceinline__ float get(int e) const {   // e known at compile time
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(u);
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+    else return __half2float(__ushort_as_half(static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)))));
+  }
+};
 
 template <typename T, int D, int BITS, bool FULL>
 __global__ void __launch_bounds__(128) paged_append_kernel(const PagedAppendArgs a) {
-  constexpr int E = D / 32, L = 1 << BITS, HP = L / 2;   // HP positive thresholds, 0 among them
-  const int lane = threadIdx.x & 31;
-  const long long v = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (v >= a.n_vec) return;
-  const bool val = blockIdx.y != 0;
-  const long long n = v / a.hkv;
-  const int kvh = static_cast<int>(v - n * a.hkv);
-  const long long slot = a.slot_map[n];
-  if (slot < 0) return;
-  if (slot >= a.n_rows) {
-    if (lane == 0) atomicOr(&g_decode_error, kErrBadPage);
-    return;
+  constexpr int LV = D / 16, VPW = 32 / LV;              // lanes per vector, vectors per warp
+  constexpr int L = 1 << BITS, HP = L / 2;               // HP non-negative thresholds, 0 among them
+  const int lane = threadIdx.x & 31, vl = lane % LV;     // the lane within its vector
+  const int kvh = blockIdx.y >> 1;
+  const bool val = blockIdx.y & 1;
+  const long long step = static_cast<long long>(gridDim.x) * 4 * VPW;
+  long long n = (static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5)) * VPW + lane / LV;
+  const long long n_warp_end = a.n_tok;
+  const T *x_base = static_cast<const T *>(val ? a.v_new : a.k_new) + static_cast<long long>(kvh) * D + 16 * vl;
+  const float *prm = (val ? a.params_v : a.params_k) + static_cast<size_t>(kvh) * 2 * D;
+  constexpr int PB = D * BITS / 8;
+
+  Raw16<T> nx{};
+  long long slot_nx = -1;
+  if (n < n_warp_end) {
+    nx.load(x_base + n * a.hkv * D);
+    slot_nx = a.slot_map[n];
   }
-  const T *src = static_cast<const T *>(val ? a.v_new : a.k_new) + v * D + E * lane;
-  float x[E];
-  load_elements<T, E>(src, x);
-  float ss = 0.f;
+  Quat ql[4], qr[4];
+  const float inv = rsqrtf(static_cast<float>(D));
 #pragma unroll
-  for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
+  for (int u = 0; u < 4; ++u) {
+    ql[u] = load_quat(prm + 8 * (4 * vl + u));
+    qr[u] = FULL ? load_quat(prm + 8 * (4 * vl + u) + 4) : Quat{1.f, 0.f, 0.f, 0.f};
+  }
+
+  for (; __any_sync(0xffffffffu, n < n_warp_end); n += step) {
+    const Raw16<T> cur = nx;
+    const bool here = n < n_warp_end;
+    const long long slot = here ? slot_nx : -1;
+    if (n + step < n_warp_end) {
+      nx.load(x_base + (n + step) * a.hkv * D);
+      slot_nx = a.slot_map[n + step];
+    }
+    const bool write = slot >= 0 && slot < a.n_rows;
+    if (slot >= a.n_rows && vl == 0) atomicOr(&g_decode_error, kErrBadPage);
+
+    float x[16];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float s = sqrtf(ss);
-  // A float32 vector whose squares leave float32's range: all in double.
-  bool extreme = false;
-  if constexpr (sizeof(T) == 4) {
-    if (ss < 1e-30f || ss > 1e30f) {
+    for (int e = 0; e < 16; ++e) x[e] = cur.get(e);
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int o = 1; o < LV; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float s = sqrtf(ss);
+    // A float32 vector whose squares leave float32's range: all in double.
+    bool extreme = false;
+    if constexpr (sizeof(T) == 4) {
       bool some = false;
 #pragma unroll
-      for (int e = 0; e < E; ++e) some |= x[e] != 0.f;
-      extreme = __any_sync(0xffffffffu, some);
+      for (int e = 0; e < 16; ++e) some |= x[e] != 0.f;
+      const unsigned any = __ballot_sync(0xffffffffu, some && (ss < 1e-30f || ss > 1e30f));
+      const unsigned mine = LV == 32 ? 0xFFFFFFFFu : ((1u << LV) - 1u) << (lane - vl);
+      extreme = (any & mine) != 0;
     }
-  }
 #pragma unroll
-  for (int hs = 1; hs < E; hs <<= 1) {
+    for (int hs = 1; hs < 16; hs <<= 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (!(e & hs)) {
-        const float p = x[e], q = x[e + hs];
-        x[e] = p + q;
-        x[e + hs] = p - q;
+      for (int e = 0; e < 16; ++e) {
+        if (!(e & hs)) {
+          const float p = x[e], q = x[e + hs];
+          x[e] = p + q;
+          x[e + hs] = p - q;
+        }
       }
     }
-  }
 #pragma unroll
-  for (int lm = 1; lm < 32; lm <<= 1) {
-    const bool upper = (lane & lm) != 0;
+    for (int lm = 1; lm < LV; lm <<= 1) {
+      const float sgn = (lane & lm) ? -1.f : 1.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float o = __shfl_xor_sync(0xffffffffu, x[e], lm);
-      x[e] = upper ? o - x[e] : x[e] + o;
+      for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], sgn, __shfl_xor_sync(0xffffffffu, x[e], lm));
     }
-  }
-  const float inv = rsqrtf(static_cast<float>(D));
-  const float *prm = (val ? a.params_v : a.params_k) + static_cast<size_t>(kvh) * 2 * D;
-  unsigned code[E], near = 0;   // near: bit e, coordinate e is decided in double
+    unsigned near = 0;            // bit e: coordinate e is decided in double
+    uint64_t codes = 0;           // code e in bits 4 e .. + 3
+    const float band = kExactBand * s;
 #pragma unroll
-  for (int u = 0; u < E / 4; ++u) {
-    const int bi = (E / 4) * lane + u;
-    const Quat w{x[4 * u] * inv, x[4 * u + 1] * inv, x[4 * u + 2] * inv, x[4 * u + 3] * inv};
-    const Quat r = block_forward(load_quat(prm + 8 * bi), load_quat(prm + 8 * bi + 4), w, FULL);
-    const float y[4] = {r.w, r.x, r.y, r.z};
+    for (int u = 0; u < 4; ++u) {
+      const Quat w{x[4 * u] * inv, x[4 * u + 1] * inv, x[4 * u + 2] * inv, x[4 * u + 3] * inv};
+      const Quat r = block_forward(ql[u], qr[u], w, FULL);
+      const float y[4] = {r.w, r.x, r.y, r.z};
+      uint32_t c4 = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float m = fabsf(y[e]);
-      float gap = m;   // distance to the nearest threshold: to 0, then to the others
-      unsigned c = 0;
-#pragma unroll
-      for (int k = 1; k < HP; ++k) {
-        const float dlt = m - a.thr[k] * s;
-        c += dlt > 0.f ? 1u : 0u;
-        gap = fminf(gap, fabsf(dlt));
+      for (int e = 0; e < 4; ++e) {
+        // m: |y|; c: positive thresholds below it, by bisection; gap: distance
+        // to the nearest threshold met, 0 among them (the nearest one is
+        // always met).
+        const float m = fabsf(y[e]);
+        float gap = m;
+        unsigned c = 0;
+        if constexpr (BITS == 2) {
+          const float d1 = m - a.thr[1] * s;
+          c = d1 > 0.f;
+          gap = fminf(gap, fabsf(d1));
+        } else if constexpr (BITS == 3) {
+          const float d2 = m - a.thr[2] * s;
+          const bool b2 = d2 > 0.f;
+          const float d1 = m - (b2 ? a.thr[3] : a.thr[1]) * s;
+          c = (b2 ? 2u : 0u) + (d1 > 0.f ? 1u : 0u);
+          gap = fminf(gap, fminf(fabsf(d2), fabsf(d1)));
+        } else {
+          const float d4 = m - a.thr[4] * s;
+          const bool b4 = d4 > 0.f;
+          const float d2 = m - (b4 ? a.thr[6] : a.thr[2]) * s;
+          const bool b2 = d2 > 0.f;
+          const float lo = b2 ? a.thr[3] : a.thr[1], hi = b2 ? a.thr[7] : a.thr[5];
+          const float d1 = m - (b4 ? hi : lo) * s;
+          c = (b4 ? 4u : 0u) + (b2 ? 2u : 0u) + (d1 > 0.f ? 1u : 0u);
+          gap = fminf(fminf(gap, fabsf(d4)), fminf(fabsf(d2), fabsf(d1)));
+        }
+        c4 |= (y[e] > 0.f ? HP + c : HP - 1 - c) << (4 * e);
+        if (gap < band) near |= 1u << (4 * u + e);
       }
-      code[4 * u + e] = y[e] > 0.f ? HP + c : HP - 1 - c;
-      if (gap < kExactBand * s) near |= 1u << (4 * u + e);
+      codes |= static_cast<uint64_t>(c4) << (16 * u);
     }
-  }
-  if (extreme) near = (1u << E) - 1u;
-  __half nrm = __float2half_rn(s);
-  const bool round_near = __half_as_ushort(__float2half_rn(s * (1.f + 4e-6f))) != __half_as_ushort(__float2half_rn(s * (1.f - 4e-6f)));
-  if (round_near || extreme || __any_sync(0xffffffffu, near != 0)) {   // warp-uniform
-    double sq = 0.0;
+    if (extreme) near = 0xFFFFu;
+    __half nrm = __float2half_rn(s);
+    const bool round_near = extreme || __half_as_ushort(__float2half_rn(s * (1.f + 4e-6f))) !=
+                                           __half_as_ushort(__float2half_rn(s * (1.f - 4e-6f)));
+    if (!write) near = 0;
+    if (__any_sync(0xffffffffu, near != 0 || (round_near && write))) {
+      double sq = 0.0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const double xe = static_cast<double>(to_f32<T>(src[e]));
-      sq = fma(xe, xe, sq);
-    }
+      for (int e = 0; e < 16; ++e) {
+        const double xe = static_cast<double>(cur.get(e));
+        sq = fma(xe, xe, sq);
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    const double s64 = sqrt(sq);
-    nrm = __double2half(s64);
-    for (unsigned lanes = __ballot_sync(0xffffffffu, near != 0); lanes; lanes &= lanes - 1) {
-      const int fl = __ffs(lanes) - 1;
-      for (unsigned es = __shfl_sync(0xffffffffu, near, fl); es; es &= es - 1) {
-        const int fe = __ffs(es) - 1, i = E * fl + fe, bi = i >> 2, rr = i & 3;
-        // the four Walsh-Hadamard outputs of block bi
-        double h[4] = {0.0, 0.0, 0.0, 0.0};
+      for (int o = 1; o < LV; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      const double s64 = sqrt(sq);
+      nrm = __double2half(s64);
+      // Each vector's lanes take one of its coordinates per turn.
+      while (__any_sync(0xffffffffu, near != 0)) {
+        const unsigned all = __ballot_sync(0xffffffffu, near != 0);
+        const unsigned mine = LV == 32 ? all : (all >> (lane - vl)) & ((1u << (LV & 31)) - 1u);
+        const int fl = mine ? __ffs(mine) - 1 : 0;                    // the lane (of the vector) that holds it
+        const unsigned es = __shfl_sync(0xffffffffu, near, lane - vl + fl);
+        const int fe = es ? __ffs(es) - 1 : 0;
+        const int i = 16 * fl + fe, bi = i >> 2, rr = i & 3;
+        double h[4] = {0.0, 0.0, 0.0, 0.0};                           // the block's Walsh-Hadamard outputs
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const double xe = static_cast<double>(to_f32<T>(src[e]));
+        for (int e = 0; e < 16; ++e) {
+          const double xe = static_cast<double>(cur.get(e));
 #pragma unroll
-          for (int c = 0; c < 4; ++c) h[c] += (__popc((4 * bi + c) & (E * lane + e)) & 1) ? -xe : xe;
+          for (int c = 0; c < 4; ++c) h[c] += (__popc((4 * bi + c) & (16 * vl + e)) & 1) ? -xe : xe;
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) h[c] += __shfl_xor_sync(0xffffffffu, h[c], o);
+          for (int o = 1; o < LV; o <<= 1) h[c] += __shfl_xor_sync(0xffffffffu, h[c], o);
         auto mul = [](const double *p, const double *q, double *r) {
           r[0] = p[0] * q[0] - p[1] * q[1] - p[2] * q[2] - p[3] * q[3];
           r[1] = p[0] * q[1] + p[1] * q[0] + p[2] * q[3] - p[3] * q[2];
           r[2] = p[0] * q[2] - p[1] * q[3] + p[2] * q[0] + p[3] * q[1];
           r[3] = p[0] * q[3] + p[1] * q[2] - p[2] * q[1] + p[3] * q[0];
         };
-        const double ql[4] = {prm[8 * bi], prm[8 * bi + 1], prm[8 * bi + 2], prm[8 * bi + 3]};
+        const double q4[4] = {prm[8 * bi], prm[8 * bi + 1], prm[8 * bi + 2], prm[8 * bi + 3]};
         double y4[4];
-        mul(ql, h, y4);
+        mul(q4, h, y4);
         if (FULL) {
-          const double qr[4] = {prm[8 * bi + 4], -static_cast<double>(prm[8 * bi + 5]),
+          const double r4[4] = {prm[8 * bi + 4], -static_cast<double>(prm[8 * bi + 5]),
                                 -static_cast<double>(prm[8 * bi + 6]), -static_cast<double>(prm[8 * bi + 7])};
           double z4[4];
-          mul(y4, qr, z4);
+          mul(y4, r4, z4);
 #pragma unroll
           for (int c = 0; c < 4; ++c) y4[c] = z4[c];
         }
         const double y = (rr == 0 ? y4[0] : rr == 1 ? y4[1] : rr == 2 ? y4[2] : y4[3]) / sqrt(static_cast<double>(D));
-        unsigned c = 0;
-#pragma unroll
+        uint64_t c = 0;
+#pragma unroll 1
         for (int k = 0; k < L - 1; ++k) c += y > a.thr64[k] * s64 ? 1u : 0u;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (lane == fl && e == fe) code[e] = c;
+        if (near != 0 && vl == fl) {
+          codes = (codes & ~(15ull << (4 * fe))) | (c << (4 * fe));
+          near &= near - 1;
+        }
       }
     }
-  }
 
-  const int mask = (1 << a.page_shift) - 1;
-  const long long at = (((slot >> a.page_shift) * a.hkv + kvh) << a.page_shift) + (slot & mask);
-  constexpr int PB = D * BITS / 8;
-  uint8_t *dst = (val ? a.pages_v : a.pages_k) + at * PB;
-  if (lane == 0) (val ? a.norms_v : a.norms_k)[at] = __half_as_ushort(nrm);
-  if constexpr (BITS == 3) {
-    constexpr int GL = 32 / E;          // lanes of a 32-code group
-    const int m0 = E * (lane & (GL - 1));
-    uint32_t w[3] = {0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int m = m0 + e;             // code m of the group
-      const uint32_t body = code[e] << (4 * (m & 7));
-#pragma unroll
-      for (int r = 0; r < 3; ++r)
-        w[r] |= m < 24 ? ((m >> 3) == r ? body : 0u) : ((code[e] >> r) & 1u) << (4 * (m & 7) + 3);
+    const int mask = (1 << a.page_shift) - 1;
+    const long long at = (((slot >> a.page_shift) * a.hkv + kvh) << a.page_shift) + (slot & mask);
+    uint8_t *dst = (val ? a.pages_v : a.pages_k) + at * PB;
+    const uint32_t c0 = static_cast<uint32_t>(codes), c1 = static_cast<uint32_t>(codes >> 32);   // codes 0..7, 8..15
+    if (write && vl == 0) (val ? a.norms_v : a.norms_k)[at] = __half_as_ushort(nrm);
+    if constexpr (BITS == 3) {
+      // Two lanes share a 32-code group: the even one holds words 0 and 1, the
+      // odd one word 2 and codes 24 .. 31, whose bit r goes to the spare bits
+      // of word r.
+      const bool odd = vl & 1;
+      const uint32_t t0 = (c1 & 0x11111111u) << 3, t1 = (c1 & 0x22222222u) << 2, t2 = (c1 & 0x44444444u) << 1;
+      const uint32_t g0 = __shfl_xor_sync(0xffffffffu, t0, 1), g1 = __shfl_xor_sync(0xffffffffu, t1, 1);
+      uint32_t *g = reinterpret_cast<uint32_t *>(dst) + 3 * (vl >> 1);
+      if (write) {
+        if (odd) {
+          g[2] = c0 | t2;
+        } else {
+          g[0] = c0 | g0;
+          g[1] = c1 | g1;
+        }
+      }
+    } else if constexpr (BITS == 4) {
+      if (write) reinterpret_cast<uint2 *>(dst)[vl] = make_uint2(c0, c1);
+    } else {
+      // 4-bit fields to 2-bit ones
+      auto squeeze = [](uint32_t v) {
+        v = (v | (v >> 2)) & 0x0F0F0F0Fu;
+        v = (v | (v >> 4)) & 0x00FF00FFu;
+        return (v | (v >> 8)) & 0xFFFFu;
+      };
+      if (write) reinterpret_cast<uint32_t *>(dst)[vl] = squeeze(c0) | (squeeze(c1) << 16);
     }
-#pragma unroll
-    for (int o = 1; o < GL; o <<= 1)
-#pragma unroll
-      for (int r = 0; r < 3; ++r) w[r] |= __shfl_xor_sync(0xffffffffu, w[r], o);
-    if ((lane & (GL - 1)) == 0) {
-      uint32_t *g = reinterpret_cast<uint32_t *>(dst) + 3 * (lane / GL);
-#pragma unroll
-      for (int r = 0; r < 3; ++r) g[r] = w[r];
-    }
-  } else {
-    constexpr int NB = E * BITS;        // bits of a lane: 8, 16, 32 or 64
-    uint64_t w = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) w |= static_cast<uint64_t>(code[e]) << (BITS * e);
-    if constexpr (NB == 8) dst[lane] = static_cast<uint8_t>(w);
-    else if constexpr (NB == 16) reinterpret_cast<uint16_t *>(dst)[lane] = static_cast<uint16_t>(w);
-    else if constexpr (NB == 32) reinterpret_cast<uint32_t *>(dst)[lane] = static_cast<uint32_t>(w);
-    else reinterpret_cast<uint64_t *>(dst)[lane] = w;
   }
 }
 
 template <typename T, int D, int BITS>
 int launch_paged_append(int variant, const PagedAppendArgs &a, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((a.n_vec + 3) / 4), 2);
+  // Up to about 8 CTAs per SM over all heads; a warp walks the rest.
+  constexpr int VPC = 4 * (512 / D);   // tokens of a CTA per turn
+  const long long turns = (a.n_tok + VPC - 1) / VPC;
+  long long gx = (8 * 148 + 2 * a.hkv - 1) / (2 * a.hkv);
+  if (gx > turns) gx = turns;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(2 * a.hkv));
   if (variant == ISOQ_FULL)
     paged_append_kernel<T, D, BITS, true><<<grid, 128, 0, st>>>(a);
   else
