@@ -622,7 +622,7 @@ int isoq_prefill_attention(const void *q_dev, int dtype, const uint8_t *packed_k
                                       B, Tq, Hq, Hkv, Tmax, d, bits, variant, params_k_dev, params_v_dev, scale,
                                       out_dev, &a);
   if (st || Tq == 0) return st;
-  return decode::run_prefill<false>(d, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
+  return decode::run_prefill<decode::kPfCausal>(d, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

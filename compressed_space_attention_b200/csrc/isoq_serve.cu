@@ -28,6 +28,7 @@ namespace decode {
 #include "prefill.cuh"
 #include "serve_any.cuh"
 #include "paged.cuh"
+#include "serve_prefix.cuh"
 
 // ---------------------------------------------------------------------------
 // Plans
@@ -72,11 +73,20 @@ struct DecodePlan {
   int64_t chunk, chunk_p;
   int splits, splits_p;
   int64_t acc_bytes, prep_bytes;     // workspace: partial states; prepared queries
+  // The prefix on tcgen05: 128-row tiles per KV head (0: the other splits),
+  // and the prepared query tiles' place in the workspace.
+  int row_tiles;
+  int64_t tiles_at;
 };
+
+// Which prefix split: rows of a KV head's batch x group from which on the
+// tcgen05 one is faster (float16 queries, 3-bit codes, d = 128 or 256).
+constexpr int kPrefixTcRows = 33;
 
 // prefix_max < 0: no prefix.  The list of a row is cut into the same splits
 // whatever its length.
-DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int64_t window, int64_t n_sink) {
+DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int64_t window, int64_t n_sink,
+                       bool prefix_tc = false) {
   DecodePlan p{};
   const int G = Hq / Hkv;
   p.share = row_share(G);
@@ -93,10 +103,23 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
     p.chunk_p = serve_chunk(static_cast<int64_t>(Hkv) * p.groups_p, tp > 0 ? tp : 32);
     p.splits_p = static_cast<int>(div_up(tp, p.chunk_p));
     prep_rows += p.groups_p;
+    if (prefix_tc) {
+      p.row_tiles = static_cast<int>(div_up(rows, kTcRows));
+      // Even splits of whole tiles, as many as fill the resident CTAs once.
+      const int64_t tiles = div_up(prefix_max, kTcTok), ctas = static_cast<int64_t>(p.row_tiles) * Hkv;
+      const int64_t slots = d == 128 ? 2 * 148 : 148;
+      int64_t splits = slots / ctas > 1 ? slots / ctas : 1;
+      if (splits > tiles) splits = tiles;
+      const int64_t per = div_up(tiles, splits > 0 ? splits : 1);
+      p.chunk_p = kTcTok * per;
+      p.splits_p = per > 0 ? static_cast<int>(div_up(tiles, per)) : 0;
+    }
   }
   p.acc_bytes = round256(static_cast<int64_t>(B) * Hq * (p.splits + p.splits_p) * (d + 2) * 4);
   const int64_t i8 = prep_rows * Hkv * decode_qprep_words(d) * 4, any = static_cast<int64_t>(B) * Hq * d * 4;
   p.prep_bytes = round256(i8 > any ? i8 : any);
+  p.tiles_at = p.acc_bytes + p.prep_bytes;
+  p.prep_bytes += static_cast<int64_t>(p.row_tiles) * Hkv * (2 * kTcRows * 2) * d;
   return p;
 }
 
@@ -175,6 +198,7 @@ int run_decode(SplitArgs &a, const DecodePlan &p, int dtype, int d, int bits, in
   a.n_zrows = p.groups;
   a.zrow_size_p = p.share_p;
   a.n_zrows_p = p.groups_p;
+  if (a.mode == kSplitWindow && p.row_tiles > 0) a.zrow_size_p = a.n_zrows_p = 0;
   a.ws_acc = static_cast<float *>(workspace);
   a.ws_ml = reinterpret_cast<float2 *>(a.ws_acc + static_cast<int64_t>(a.batch) * a.hq * a.slot_stride * d);
   unsigned char *prep = static_cast<unsigned char *>(workspace) + p.acc_bytes;
@@ -183,7 +207,11 @@ int run_decode(SplitArgs &a, const DecodePlan &p, int dtype, int d, int bits, in
   CodebookF32 cb;
   codebook_f32(d, bits, &cb);
   for (int j = 0; j < 16; ++j) a.centroid[j] = j < cb.levels ? cb.centroid[j] : 0.f;
-  int e;
+  int e = ISOQ_OK;
+  // The prefix on tcgen05: its query tiles first, its split last, so that it
+  // runs beside the split over the rows' own caches.
+  if (p.row_tiles > 0) e = run_prep_prefix(d, variant, a, static_cast<unsigned char *>(workspace) + p.tiles_at, p.row_tiles, st);
+  if (e) return e;
   if (i8 && dtype == ISOQ_F16 && bits == 3 && (d == 128 || d == 256)) {
     if (d == 128)
       e = variant == ISOQ_FULL ? run_i8_rows<128, true>(a, st) : run_i8_rows<128, false>(a, st);
@@ -193,6 +221,9 @@ int run_decode(SplitArgs &a, const DecodePlan &p, int dtype, int d, int bits, in
     e = run_prep_rotate(dtype, d, variant, a, st);
     if (e == ISOQ_OK) e = run_split_any(d, bits, a, st);
   }
+  if (e == ISOQ_OK && p.row_tiles > 0)
+    e = run_prefix_tc(d, a, static_cast<unsigned char *>(workspace) + p.tiles_at, p.row_tiles, p.splits_p,
+                      static_cast<int>(p.chunk_p), st);
   if (e) return e;
   CombineArgs c;
   c.params_v = params_v;
@@ -231,8 +262,15 @@ size_t isoq_decode_prefix_workspace_size(int B, int Hq, int Hkv, int64_t prefix_
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Tmax <= 0 || Tmax >= (1ll << 31) || prefix_tokens < 0 ||
       prefix_tokens >= (1ll << 31) || !supported_d(d) || Hq % Hkv)
     return 0;
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0);
-  return static_cast<size_t>(p.acc_bytes + p.prep_bytes);
+  // The larger of the two plans (which one runs also depends on types and
+  // alignment).
+  size_t need = 0;
+  for (const bool tc : {false, true}) {
+    const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0, tc);
+    const size_t n = static_cast<size_t>(p.acc_bytes + p.prep_bytes);
+    need = n > need ? n : need;
+  }
+  return need;
 }
 
 int isoq_decode_attention_window(const void *q_dev, int dtype, const uint8_t *packed_k_dev,
@@ -300,11 +338,22 @@ int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *pr
       !decode::aligned(norms_v_dev, 2) || !decode::aligned(prefix_norms_k_dev, 2) ||
       !decode::aligned(prefix_norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4) || !decode::aligned(prefix_len_dev, 4))
     return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0);
+  // The tcgen05 split reads codes and norms by plain loads: any prefix does.
+  const bool tc = decode::tc_prefix(dtype, d, bits) && B * static_cast<int64_t>(Hq / Hkv) >= decode::kPrefixTcRows &&
+                  prefix_tokens > 0;
+  // The integer split rounds a copy of norms up to 8 tokens: within the room
+  // of the last KV head only where the prefix's tokens are a multiple of 8.
+  const bool i8 = decode::i8_cache(norms_k_dev, norms_v_dev, Tmax) &&
+                  (tc || (decode::i8_cache(prefix_norms_k_dev, prefix_norms_v_dev, prefix_head_stride) &&
+                          prefix_tokens % 8 == 0));
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0, tc);
+  if (workspace_bytes < isoq_decode_prefix_workspace_size(B, Hq, Hkv, prefix_tokens, Tmax, d) || !workspace_dev)
+    return set_error(ISOQ_ERR_INVALID_ARG, "workspace is NULL or too small: %zu < %zu", workspace_bytes,
+                     isoq_decode_prefix_workspace_size(B, Hq, Hkv, prefix_tokens, Tmax, d));
   st = decode::check_workspace(workspace_dev, workspace_bytes, p);
   if (st) return st;
   decode::SplitArgs a{};
-  a.mode = decode::kSplitPrefix;
+  a.mode = tc ? decode::kSplitWindow : decode::kSplitPrefix;
   a.q = q_dev;
   a.packed_k = packed_k_dev;
   a.packed_v = packed_v_dev;
@@ -326,10 +375,6 @@ int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *pr
   a.prefix_len = prefix_len_dev;
   a.prefix_max = prefix_tokens;
   a.head_stride = prefix_head_stride;
-  // A copy of norms is rounded up to 8 tokens: within the room of the last
-  // KV head only where the prefix's tokens are a multiple of 8.
-  const bool i8 = decode::i8_cache(norms_k_dev, norms_v_dev, Tmax) &&
-                  decode::i8_cache(prefix_norms_k_dev, prefix_norms_v_dev, prefix_head_stride) && prefix_tokens % 8 == 0;
   return decode::run_decode(a, p, dtype, d, bits, variant, i8, params_v_dev, out_dev, workspace_dev,
                             reinterpret_cast<cudaStream_t>(stream));
 }
@@ -401,7 +446,7 @@ int isoq_prefill_attention_window(const void *q_dev, int dtype, const uint8_t *p
   if (Tq == 0) return ISOQ_OK;
   a.window = decode::clamp31(window);
   a.n_sink = decode::clamp31(n_sink);
-  return decode::run_prefill<true>(d, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
+  return decode::run_prefill<decode::kPfWindow>(d, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int isoq_build_block_tables(const int32_t *seq_lens_dev, const int32_t *new_lens_dev, const int32_t *free_pages_dev,

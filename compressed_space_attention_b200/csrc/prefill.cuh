@@ -70,8 +70,22 @@ struct PrefillArgs {
   float out_unit;                 // 1 / (alpha * d)
   uint32_t lut_lo0, lut_lo1, lut_hi0, lut_hi1;   // float16 alpha c_k, low / high bytes
   uint32_t res_lo0, res_lo1, res_hi0, res_hi1;   // float16 alpha c_k - fp16(alpha c_k), low / high bytes
-  int window, n_sink;             // WIN: tokens j > p - window or j < n_sink only
+  int window, n_sink;             // kPfWindow: tokens j > p - window or j < n_sink only
+  // kPfPrefix: query rows prepared in the operand layout, [Hkv][row tiles] of
+  // float16 hi and lo tiles; partial states as the decode's splits write them.
+  const unsigned char *q_tiles;
+  const int32_t *prefix_len;
+  long long head_stride;          // tokens between KV heads
+  int row_tiles, chunk;           // 128-row tiles per KV head; tokens per split
+  float *ws_acc;
+  float2 *ws_ml;
+  int slot_stride;
+  float acc_unit;                 // 1 / (alpha sqrt(d))
 };
+
+// What the kernel computes: the causal chunk, the same under a sliding window
+// with sinks, or partial states of a batch's queries over one shared prefix.
+enum PrefillKind { kPfCausal = 0, kPfWindow = 1, kPfPrefix = 2 };
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -130,7 +144,7 @@ struct TcCfg {
   // 1024-byte boundary and reports kErrSmemAlign otherwise.
   static constexpr int MIN_BLOCKS = D == 128 ? 2 : 1;
   static constexpr int SLACK = MIN_BLOCKS == 2 ? 0 : 1024;
-  static constexpr int SMEM = OFF_BAR + 8 * 3 + 8 + SLACK;
+  static constexpr int SMEM = OFF_BAR + 8 * 4 + 8 + SLACK;
   static constexpr int TMEM_COLS = D == 128 ? 256 : 512;     // S (2 x 64) + O (D), rounded to a power of 2
   static_assert(32 * D * 4 <= 2 * KV_BYTES, "prep scratch (32 rows) fits the K and K-residual tiles");
   static_assert(MIN_BLOCKS * (SMEM + 1024) <= 233472, "shared memory per SM (1 KB reserved per CTA)");
@@ -202,13 +216,20 @@ __device__ __forceinline__ void tc_expand(const TcCodes<D> &c, unsigned char *ti
   }
 }
 
-// WIN: a sliding window with sink tokens.  The query at position p sees j <= p
+// kPfWindow: a sliding window with sink tokens.  The query at position p sees j <= p
 // with j > p - window or j < n_sink.  The CTA's tiles are the sink tiles, then
 // those from the first row's window on; a tile that some row of a warp does
 // not see whole is masked by column.
-template <typename T, int D, bool FULL, int GP, bool WIN = false>
+//
+// kPfPrefix: the rows are the query heads of all batch rows (row r of a KV
+// head: batch row r / G, head r mod G), rotated and split beforehand
+// (prep_prefix_kernel) and fetched by two bulk copies; every row sees all of
+// the CTA's tokens, a chunk of the prefix; instead of outputs the epilogue
+// writes one partial state (m, l, acc) per row.  Grid (row tiles, Hkv, splits).
+template <typename T, int D, bool FULL, int GP, int KIND = kPfCausal>
 __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_kernel(const PrefillArgs a) {
   using C = TcCfg<D>;
+  constexpr bool WIN = KIND == kPfWindow, PREFIX = KIND == kPfPrefix;
   constexpr int BQ = kTcRows / GP;
   constexpr int QBLK = kTcRows * 128, KBLK = kTcTok * 128;
   extern __shared__ unsigned char smem_raw[];
@@ -225,7 +246,8 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   float *nrm_s = reinterpret_cast<float *>(smem + C::OFF_NORM);   // [2][kTcTok] s^K score_unit, s^V of the tile in the softmax
   uint64_t *bar_s = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);   // [2]: S buffer b's product done
   uint64_t *bar_o = bar_s + 2;                                          // PV product done
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_o + 1);
+  uint64_t *bar_q = bar_o + 1;                                          // kPfPrefix: the query tiles
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_q + 1);
   // A product wait that gave up in iteration j sets fail_s[j % 2]; it is read
   // after the iteration's last block barrier (see the loop).
   volatile uint8_t *fail_s = reinterpret_cast<volatile uint8_t *>(tmem_slot + 1);
@@ -235,16 +257,24 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   const int tid = threadIdx.x, warp = tid >> 5;
   const int G = a.group;
 
-  int len = a.seq_lens[b];
+  const int32_t *lens = PREFIX ? a.prefix_len : a.seq_lens + b;
+  int len = *lens;
   len = len < 0 ? 0 : (len > a.tmax ? static_cast<int>(a.tmax) : len);
-  const int pos_base = a.seq_lens[b] - a.tq;
-  const int tq0 = qt * BQ;
-  const int p_first = pos_base + tq0;
+  const int pos_base = PREFIX ? 0 : *lens - a.tq;
+  const int tq0 = PREFIX ? 0 : qt * BQ;
+  const int p_first = PREFIX ? 0x7FFFFF00 : pos_base + tq0;   // (every token is at or before it)
   int p_last = pos_base + tq0 + BQ - 1;
   if (tq0 + BQ > a.tq) p_last = pos_base + a.tq - 1;
   int tend = p_last + 1 < len ? p_last + 1 : len;
   if (tend < 0) tend = 0;
   int n_tiles = (tend + kTcTok - 1) / kTcTok;
+  int t_base = 0;   // kPfPrefix: the split's first token
+  if constexpr (PREFIX) {
+    const long long first = static_cast<long long>(b) * a.chunk;
+    t_base = first < len ? static_cast<int>(first) : len;
+    tend = len - t_base > a.chunk ? t_base + a.chunk : len;
+    n_tiles = (tend - t_base + kTcTok - 1) / kTcTok;
+  }
   // WIN: tiles [0, n_sink_tiles), then from win_tile on.
   int n_sink_tiles = 0, win_tile = 0;
   if constexpr (WIN) {
@@ -262,14 +292,14 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     if constexpr (WIN)
       return kTcTok * (j < n_sink_tiles ? j : j - n_sink_tiles + win_tile);
     else
-      return kTcTok * j;
+      return t_base + kTcTok * j;
   };
 
-  const long long pair = static_cast<long long>(b) * a.hkv + kvh;
-  const uint8_t *kb = a.packed_k + pair * a.tmax * C::PB;
-  const uint8_t *vb = a.packed_v + pair * a.tmax * C::PB;
-  const uint16_t *nkb = a.norms_k + pair * a.tmax;
-  const uint16_t *nvb = a.norms_v + pair * a.tmax;
+  const long long cache0 = PREFIX ? kvh * a.head_stride : (static_cast<long long>(b) * a.hkv + kvh) * a.tmax;
+  const uint8_t *kb = a.packed_k + cache0 * C::PB;
+  const uint8_t *vb = a.packed_v + cache0 * C::PB;
+  const uint16_t *nkb = a.norms_k + cache0;
+  const uint16_t *nvb = a.norms_v + cache0;
 
   // Codes and norms of upcoming tiles, one phase ahead, in registers:
   // kc = the next K tile to expand, vc = the next V tile, nrm = the norm
@@ -296,10 +326,19 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     mbar_init(&bar_s[0], 1);
     mbar_init(&bar_s[1], 1);
     mbar_init(bar_o, 1);
+    mbar_init(bar_q, 1);
     fail_s[0] = fail_s[1] = 0;
     mbar_fence_init();
   }
-
+  if constexpr (PREFIX) {
+    // The prepared query tiles; a wait that gives up counts as a product's.
+    if (tid == 0) {
+      const unsigned char *src = a.q_tiles + (static_cast<long long>(kvh) * a.row_tiles + qt) * (2 * C::Q_BYTES);
+      mbar_arrive_expect_tx(bar_q, 2 * C::Q_BYTES);
+      bulk_load(q_hi, src, C::Q_BYTES, bar_q);
+      bulk_load(q_lo, src + C::Q_BYTES, C::Q_BYTES, bar_q);
+    }
+  } else {
   // ---- prep, 32 rows per pass: rotate, split into float16 hi / lo (SW128 K-major) ----
   for (int pass = 0; pass < kTcRows / 32; ++pass) {
     for (int i = tid; i < 32 * D; i += kTcThreads) {
@@ -330,6 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
       *reinterpret_cast<uint4 *>(q_lo + tc_off(m, 8 * c, QBLK)) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
     }
     __syncthreads();
+  }
   }
   tc_fence_before();
   __syncthreads();
@@ -382,6 +422,12 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   bool failed = false;
   int qk_issued = 0, qk_done = 0, o_issued = 0, o_done = 0;
 
+  if constexpr (PREFIX) {
+    if (__syncthreads_or(!mbar_wait_bounded(bar_q, 0))) {
+      failed = true;
+      n_tiles = 0;
+    }
+  }
   if (n_tiles > 0) {
     store_norm();
     if (n_tiles > 1) fetch_norm(1);
@@ -571,6 +617,38 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
         if (!mbar_wait_bounded(&bar_s[j & 1], (j >> 1) & 1)) break;
       if (o_issued > o_done) mbar_wait_bounded(bar_o, o_done & 1);
     }
+  } else if constexpr (PREFIX) {
+    // ---- epilogue: one partial state per row ----
+    tc_fence_after();
+    __syncthreads();
+    float *xchg = reinterpret_cast<float *>(q_hi);   // [2][kTcRows] row sums; the query tiles are free
+    float l0, l1;
+    f2_unpack(l2, l0, l1);
+    xchg[half * kTcRows + r] = l0 + l1;
+    __syncthreads();
+    const int row = kTcRows * qt + r;
+    const bool live = row < a.batch * a.group;
+    const long long query = live ? static_cast<long long>(row / a.group) * a.hq + kvh * a.group + row % a.group : 0;
+    const long long slot = query * a.slot_stride + b;
+#pragma unroll 1
+    for (int c = 0; c < OH / 16; ++c) {
+      float v[16];
+      if (n_tiles > 0) {
+        tc_ld16(t_o + OH * half + lane_off + 16 * c, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+      }
+      if (live) {
+        float4 *dst = reinterpret_cast<float4 *>(a.ws_acc + slot * D + OH * half + 16 * c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          dst[j] = make_float4(v[4 * j] * a.acc_unit, v[4 * j + 1] * a.acc_unit, v[4 * j + 2] * a.acc_unit,
+                               v[4 * j + 3] * a.acc_unit);
+      }
+    }
+    if (live && half == 0)
+      a.ws_ml[slot] = make_float2(mx == -INFINITY ? -INFINITY : mx * 0.69314718055994531f, xchg[r] + xchg[kTcRows + r]);
   } else {
     // ---- epilogue, 32 rows per pass: O / l from TMEM, rotate back, store ----
     tc_fence_after();
@@ -613,14 +691,17 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   }
   tc_fence_before();
   __syncthreads();
+  // kPfPrefix overlaps the split over the rows' own caches, launched before
+  // it; the combine waits for this grid, so this grid ends after that one.
+  if constexpr (PREFIX) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
 }
 
-template <typename T, int D, bool FULL, int GP, bool WIN>
+template <typename T, int D, bool FULL, int GP, int KIND>
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
   using C = TcCfg<D>;
-  auto kernel = prefill_tc_kernel<T, D, FULL, GP, WIN>;
+  auto kernel = prefill_tc_kernel<T, D, FULL, GP, KIND>;
   static bool configured = false;
   static std::mutex mu;
   {
@@ -697,25 +778,25 @@ inline const PfTables &pf_tables() {
   return tb;
 }
 
-template <typename T, int D, bool FULL, bool WIN>
+template <typename T, int D, bool FULL, int KIND>
 int run_prefill_g(const PrefillArgs &a, cudaStream_t st) {
   switch (a.group) {
-    case 1: return launch_prefill_tc<T, D, FULL, 1, WIN>(a, st);
-    case 2: return launch_prefill_tc<T, D, FULL, 2, WIN>(a, st);
-    case 4: return launch_prefill_tc<T, D, FULL, 4, WIN>(a, st);
-    default: return launch_prefill_tc<T, D, FULL, 8, WIN>(a, st);
+    case 1: return launch_prefill_tc<T, D, FULL, 1, KIND>(a, st);
+    case 2: return launch_prefill_tc<T, D, FULL, 2, KIND>(a, st);
+    case 4: return launch_prefill_tc<T, D, FULL, 4, KIND>(a, st);
+    default: return launch_prefill_tc<T, D, FULL, 8, KIND>(a, st);
   }
 }
 
-template <typename T, bool WIN>
+template <typename T, int KIND>
 int run_prefill_t(int d, int variant, const PrefillArgs &a, cudaStream_t st) {
   if (d == 128)
-    return variant == ISOQ_FULL ? run_prefill_g<T, 128, true, WIN>(a, st) : run_prefill_g<T, 128, false, WIN>(a, st);
-  return variant == ISOQ_FULL ? run_prefill_g<T, 256, true, WIN>(a, st) : run_prefill_g<T, 256, false, WIN>(a, st);
+    return variant == ISOQ_FULL ? run_prefill_g<T, 128, true, KIND>(a, st) : run_prefill_g<T, 128, false, KIND>(a, st);
+  return variant == ISOQ_FULL ? run_prefill_g<T, 256, true, KIND>(a, st) : run_prefill_g<T, 256, false, KIND>(a, st);
 }
 
-template <bool WIN>
-int run_prefill(int d, int variant, PrefillArgs a, cudaStream_t st) {
+// The kernel's tables and units of alpha.
+inline void prefill_tables(PrefillArgs &a, int d) {
   const PfTables &tb = pf_tables();
   a.lut_lo0 = tb.lo0;
   a.lut_lo1 = tb.lo1;
@@ -726,8 +807,14 @@ int run_prefill(int d, int variant, PrefillArgs a, cudaStream_t st) {
   a.res_hi0 = tb.rhi0;
   a.res_hi1 = tb.rhi1;
   a.out_unit = static_cast<float>(1.0 / (tb.alpha * d));
+  a.acc_unit = static_cast<float>(1.0 / (tb.alpha * std::sqrt(static_cast<double>(d))));
   a.score_unit = static_cast<float>(a.score_unit / (tb.alpha * std::sqrt(static_cast<double>(d))));
-  return run_prefill_t<__half, WIN>(d, variant, a, st);
+}
+
+template <int KIND>
+int run_prefill(int d, int variant, PrefillArgs a, cudaStream_t st) {
+  prefill_tables(a, d);
+  return run_prefill_t<__half, KIND>(d, variant, a, st);
 }
 
 // Checks the arguments of a prefill entry point and fills in the kernel's.
