@@ -28,6 +28,7 @@ namespace decode {
 #include "prefill.cuh"
 #include "serve_any.cuh"
 #include "paged.cuh"
+#include "rows_tc.cuh"
 #include "serve_prefix.cuh"
 
 // ---------------------------------------------------------------------------
@@ -73,8 +74,8 @@ struct DecodePlan {
   int64_t chunk, chunk_p;
   int splits, splits_p;
   int64_t acc_bytes, prep_bytes;     // workspace: partial states; prepared queries
-  // The prefix on tcgen05: 128-row tiles per KV head (0: the other splits),
-  // and the prepared query tiles' place in the workspace.
+  // The prefix on tcgen05: 128-row tiles per KV head (0: the other splits);
+  // at d = 256 the prepared query tiles' place in the workspace.
   int row_tiles;
   int64_t tiles_at;
 };
@@ -105,13 +106,14 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
     prep_rows += p.groups_p;
     if (prefix_tc) {
       p.row_tiles = static_cast<int>(div_up(rows, kTcRows));
-      // Even splits of whole tiles, as many as fill the resident CTAs once.
-      const int64_t tiles = div_up(prefix_max, kTcTok), ctas = static_cast<int64_t>(p.row_tiles) * Hkv;
-      const int64_t slots = d == 128 ? 2 * 148 : 148;
+      // Even splits of whole tiles, as many as fill the resident CTAs (one
+      // per SM) once.
+      const int64_t tok = d == 128 ? kRowsTok : kTcTok, tiles = div_up(prefix_max, tok);
+      const int64_t ctas = static_cast<int64_t>(p.row_tiles) * Hkv, slots = 148;
       int64_t splits = slots / ctas > 1 ? slots / ctas : 1;
       if (splits > tiles) splits = tiles;
       const int64_t per = div_up(tiles, splits > 0 ? splits : 1);
-      p.chunk_p = kTcTok * per;
+      p.chunk_p = tok * per;
       p.splits_p = per > 0 ? static_cast<int>(div_up(tiles, per)) : 0;
     }
   }
@@ -119,7 +121,7 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
   const int64_t i8 = prep_rows * Hkv * decode_qprep_words(d) * 4, any = static_cast<int64_t>(B) * Hq * d * 4;
   p.prep_bytes = round256(i8 > any ? i8 : any);
   p.tiles_at = p.acc_bytes + p.prep_bytes;
-  p.prep_bytes += static_cast<int64_t>(p.row_tiles) * Hkv * (2 * kTcRows * 2) * d;
+  if (d != 128) p.prep_bytes += static_cast<int64_t>(p.row_tiles) * Hkv * (2 * kTcRows * 2) * d;
   return p;
 }
 
@@ -210,7 +212,7 @@ int run_decode(SplitArgs &a, const DecodePlan &p, int dtype, int d, int bits, in
   int e = ISOQ_OK;
   // The prefix on tcgen05: its query tiles first, its split last, so that it
   // runs beside the split over the rows' own caches.
-  if (p.row_tiles > 0) e = run_prep_prefix(d, variant, a, static_cast<unsigned char *>(workspace) + p.tiles_at, p.row_tiles, st);
+  if (p.row_tiles > 0 && d != 128) e = run_prep_prefix(d, variant, a, static_cast<unsigned char *>(workspace) + p.tiles_at, p.row_tiles, st);
   if (e) return e;
   if (i8 && dtype == ISOQ_F16 && bits == 3 && (d == 128 || d == 256)) {
     if (d == 128)
@@ -222,7 +224,7 @@ int run_decode(SplitArgs &a, const DecodePlan &p, int dtype, int d, int bits, in
     if (e == ISOQ_OK) e = run_split_any(d, bits, a, st);
   }
   if (e == ISOQ_OK && p.row_tiles > 0)
-    e = run_prefix_tc(d, a, static_cast<unsigned char *>(workspace) + p.tiles_at, p.row_tiles, p.splits_p,
+    e = run_prefix_tc(d, variant, a, static_cast<unsigned char *>(workspace) + p.tiles_at, p.row_tiles, p.splits_p,
                       static_cast<int>(p.chunk_p), st);
   if (e) return e;
   CombineArgs c;
@@ -446,7 +448,11 @@ int isoq_prefill_attention_window(const void *q_dev, int dtype, const uint8_t *p
   if (Tq == 0) return ISOQ_OK;
   a.window = decode::clamp31(window);
   a.n_sink = decode::clamp31(n_sink);
-  return decode::run_prefill<decode::kPfWindow>(d, block_map_variant(variant), a, reinterpret_cast<cudaStream_t>(stream));
+  variant = block_map_variant(variant);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // The 128-row kernel moves rows 8 bytes at a time.
+  if (d == 128 && decode::aligned(q_dev, 8) && decode::aligned(out_dev, 8)) return decode::run_window_rows(variant, a, s);
+  return decode::run_prefill<decode::kPfWindow>(d, variant, a, s);
 }
 
 int isoq_build_block_tables(const int32_t *seq_lens_dev, const int32_t *new_lens_dev, const int32_t *free_pages_dev,

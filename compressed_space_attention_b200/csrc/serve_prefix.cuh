@@ -74,8 +74,8 @@ int launch_prep_prefix(int variant, const SplitArgs &a, unsigned char *tiles, in
 }
 
 int run_prep_prefix(int d, int variant, const SplitArgs &a, unsigned char *tiles, int row_tiles, cudaStream_t st) {
-  return d == 128 ? launch_prep_prefix<128>(variant, a, tiles, row_tiles, st)
-                  : launch_prep_prefix<256>(variant, a, tiles, row_tiles, st);
+  (void)d;   // 256: at d = 128 the kernel prepares its queries itself
+  return launch_prep_prefix<256>(variant, a, tiles, row_tiles, st);
 }
 
 template <int D>
@@ -89,9 +89,11 @@ int launch_prefix_tc(const PrefillArgs &p, int splits, cudaStream_t st) {
   return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "prefix launch: %s", cudaGetErrorString(e));
 }
 
-int run_prefix_tc(int d, const SplitArgs &a, const unsigned char *tiles, int row_tiles, int splits, int chunk,
-                  cudaStream_t st) {
+int run_prefix_tc(int d, int variant, const SplitArgs &a, const unsigned char *tiles, int row_tiles, int splits,
+                  int chunk, cudaStream_t st) {
   PrefillArgs p{};
+  p.q = a.q;
+  p.params_k = a.params_k;
   p.packed_k = a.prefix_k;
   p.packed_v = a.prefix_v;
   p.norms_k = a.prefix_nk;
@@ -111,5 +113,15 @@ int run_prefix_tc(int d, const SplitArgs &a, const unsigned char *tiles, int row
   p.slot_stride = a.slot_stride;
   p.score_unit = static_cast<float>(a.scale * 1.4426950408889634);
   prefill_tables(p, d);
-  return d == 128 ? launch_prefix_tc<128>(p, splits, st) : launch_prefix_tc<256>(p, splits, st);
+  if (d == 256) return launch_prefix_tc<256>(p, splits, st);
+  const dim3 grid(static_cast<unsigned>(row_tiles), static_cast<unsigned>(a.hkv), static_cast<unsigned>(splits));
+  return variant == ISOQ_FULL ? launch_rows_tc<kPfPrefix, true>(p, grid, st) : launch_rows_tc<kPfPrefix, false>(p, grid, st);
+}
+
+// Windowed chunked prefill at d = 128.
+int run_window_rows(int variant, PrefillArgs a, cudaStream_t st) {
+  prefill_tables(a, 128);
+  const int per = kTcRows / a.group;
+  const dim3 grid(static_cast<unsigned>((a.tq + per - 1) / per), static_cast<unsigned>(a.hkv), static_cast<unsigned>(a.batch));
+  return variant == ISOQ_FULL ? launch_rows_tc<kPfWindow, true>(a, grid, st) : launch_rows_tc<kPfWindow, false>(a, grid, st);
 }
