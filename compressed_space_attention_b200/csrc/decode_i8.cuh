@@ -488,29 +488,36 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
   const int n_rounds = (n_blk + kI8Warps - 1) / kI8Warps;
   auto issue = [&](int r) {
     if constexpr (MODE == kSplitPaged) {
-      // Every lane of one warp: lane (unit, tensor) copies one page's share
-      // of one tensor (16 or 32 tokens); whole shares, tokens past the end
-      // of the row among them, since a page is always there whole.
+      // Every lane of one warp: lane (unit, tensor), a unit being a block, or
+      // half of one where a page holds 16 tokens.  The first unit of a run
+      // within one page copies the run, one tensor per lane; whole units,
+      // tokens past the end of the row among them, since a page is always
+      // there whole.
       const int s = r % kI8Stages, u0 = kI8Warps * r << unit_shift;
       int units = (n_blk << unit_shift) - u0;
       units = units > kI8Warps << unit_shift ? kI8Warps << unit_shift : units;
       const int ut = kBlk >> unit_shift;         // tokens of a unit
-      const int u = lane >> 2, which = lane & 3;
-      const int page = u < units ? page_of[u0 + u] : -1;
+      const int u = lane >> 2, which = lane & 3, v = v0 + kI8Warps * r + (u >> unit_shift);
+      const int page = u < units ? page_of[u0 + u] : -1, blk = block_at(v);
+      const bool first = page >= 0 && (unit_shift || u == 0 || (blk & ((1 << (a.page_shift - 5)) - 1)) == 0 ||
+                                       blk != block_at(v - 1) + 1);
+      const unsigned firsts = __ballot_sync(0xffffffffu, first && which == 0);
       const int live = __popc(__ballot_sync(0xffffffffu, page >= 0 && which == 0));
+      const unsigned above = firsts & ~((2u << (4 * u)) - 1u);
+      const int n = unit_shift ? ut : ((above ? (__ffs(above) - 1) >> 2 : units) - u) * ut;   // tokens of the run
       unsigned char *st = ring + s * C::ROUND_BYTES;
       if (lane == 0) {
         *rounds_issued = static_cast<uint32_t>(r + 1);
         mbar_arrive_expect_tx(&full_bar[s], static_cast<uint32_t>(live * ut * (2 * C::PB + 4)));
       }
       __syncwarp();
-      if (page >= 0) {
-        const int t = kBlk * block_at(v0 + kI8Warps * r + (u >> unit_shift)) + 16 * (u & unit_shift);
+      if (first) {
+        const int t = kBlk * blk + 16 * (u & unit_shift);
         const long long at = ((static_cast<long long>(page) * a.hkv + kvh) << a.page_shift) + (t & ((1 << a.page_shift) - 1));
-        if (which == 0) bulk_load(st + u * ut * C::PB, a.packed_k + at * C::PB, ut * C::PB, &full_bar[s]);
-        else if (which == 1) bulk_load(st + C::R_V + u * ut * C::PB, a.packed_v + at * C::PB, ut * C::PB, &full_bar[s]);
-        else if (which == 2) bulk_load(st + C::R_NK + u * ut * 2, a.norms_k + at, ut * 2, &full_bar[s]);
-        else bulk_load(st + C::R_NV + u * ut * 2, a.norms_v + at, ut * 2, &full_bar[s]);
+        if (which == 0) bulk_load(st + u * ut * C::PB, a.packed_k + at * C::PB, n * C::PB, &full_bar[s]);
+        else if (which == 1) bulk_load(st + C::R_V + u * ut * C::PB, a.packed_v + at * C::PB, n * C::PB, &full_bar[s]);
+        else if (which == 2) bulk_load(st + C::R_NK + u * ut * 2, a.norms_k + at, n * 2, &full_bar[s]);
+        else bulk_load(st + C::R_NV + u * ut * 2, a.norms_v + at, n * 2, &full_bar[s]);
       }
       return;
     } else if constexpr (LISTED) {

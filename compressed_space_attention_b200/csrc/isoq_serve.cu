@@ -48,17 +48,24 @@ inline int64_t most_blocks(int64_t tmax, int64_t window, int64_t n_sink) {
   return near < all && sink < all && near + sink < all ? near + sink : all;
 }
 
-// Tokens per split for `ctas` row groups of `tokens` listed tokens each.
-inline int64_t serve_chunk(int64_t ctas, int64_t tokens) {
-  static constexpr int64_t kChunks[] = {4096, 2048, 1536, 1024, 768, 512, 256, 128};
+// Tokens per split for `ctas` row groups of up to `tokens` listed tokens each:
+// the chunk that minimises the wave model of decode_chunk_tokens (4 CTAs
+// resident per SM, k of them moving k / (k + 0.7) of its full rate, a CTA
+// costing about 160 tokens' worth of set-up and merge), over finer chunks, down
+// to one round of 128 tokens (1 row x 1,028 tokens x 4 KV heads: 10.3 us at
+// 128 tokens per split, 16.4 at 512).  Without a window the rows are taken to
+// fill three quarters of the longest, ragged as they are (16 rows of 8,192 to
+// 16,384 tokens, 8 KV heads: 121 us at 1,024 tokens per split, 134 at the 2,048
+// that full rows would suggest).
+inline int64_t serve_chunk(int64_t ctas, int64_t tokens, bool ragged) {
+  static constexpr int64_t kChunks[] = {4096, 2560, 2048, 1536, 1280, 1024, 896, 768, 640, 512, 384, 256, 128};
   constexpr int64_t kSms = 148, kSlots = 4, kCtaCost = 160;
   int64_t best_chunk = kChunks[0], best_cost = -1;
   for (const int64_t c : kChunks) {
-    const int64_t splits = div_up(tokens, c);
-    int64_t m = div_up(ctas * splits, kSms), phases10 = 0;
-    const int64_t full = m / kSlots;
-    phases10 = full * (10 * kSlots + 7);
-    if (m % kSlots) phases10 += 10 * (m % kSlots) + 7;
+    int64_t n = ctas * div_up(tokens, c);
+    if (ragged && tokens > c) n = (3 * n + 3) / 4;
+    const int64_t m = div_up(n, kSms), full = m / kSlots, rest = m % kSlots;
+    const int64_t phases10 = full * (10 * kSlots + 7) + (rest ? 10 * rest + 7 : 0);
     const int64_t cost = phases10 * ((c < tokens ? c : tokens) + kCtaCost);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
@@ -93,7 +100,7 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
   p.share = row_share(G);
   p.groups = static_cast<int>(div_up(G, p.share));
   const int64_t tokens = 32 * most_blocks(tmax, window, n_sink);
-  p.chunk = serve_chunk(static_cast<int64_t>(B) * Hkv * p.groups, tokens);
+  p.chunk = serve_chunk(static_cast<int64_t>(B) * Hkv * p.groups, tokens, window >= tmax);
   p.splits = static_cast<int>(div_up(tokens, p.chunk));
   int64_t prep_rows = static_cast<int64_t>(B) * p.groups;
   if (prefix_max >= 0) {
@@ -101,7 +108,7 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
     p.share_p = row_share(static_cast<int>(rows < 8 ? rows : 8));
     p.groups_p = static_cast<int>(div_up(rows, p.share_p));
     const int64_t tp = 32 * div_up(prefix_max, 32);
-    p.chunk_p = serve_chunk(static_cast<int64_t>(Hkv) * p.groups_p, tp > 0 ? tp : 32);
+    p.chunk_p = serve_chunk(static_cast<int64_t>(Hkv) * p.groups_p, tp > 0 ? tp : 32, false);
     p.splits_p = static_cast<int>(div_up(tp, p.chunk_p));
     prep_rows += p.groups_p;
     if (prefix_tc) {

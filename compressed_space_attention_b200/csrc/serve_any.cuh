@@ -9,18 +9,20 @@
 // combine_kernel.
 //
 // A CTA's four warps take the split's 32-token blocks in turn, up to RG query
-// rows at once, so that one unpacking of a code serves all of them.  For the
-// scores a lane is a token: it reads its packed row from shared memory 16
-// bytes at a time (row stride an odd number of 16-byte units: no bank
-// conflicts), looks each code up in a table of (c, c) pairs and multiplies it
-// with the query rows, two rows per f32x2 instruction, the query values
-// broadcast from shared memory.  For the values a lane is d / 32 dimensions
-// and the loop runs over the tokens, their weights broadcast.  The next block
-// arrives by 16-byte asynchronous copies (two stages per warp).
+// rows at once, so that one unpacking of a code serves all of them.  The next
+// block arrives by 16-byte asynchronous copies (two stages per warp; a row's
+// stride is an odd number of 16-byte units: no bank conflicts).
+//   Scores: lane (t, s) = (lane mod 8, lane / 8) takes tokens t, t + 8, t + 16,
+//   t + 24 and the 32-code groups s, s + 4, ...: every query value it loads
+//   (RG rows of one dimension, broadcast over t) serves four tokens, every
+//   centroid it looks up RG rows, two per f32x2 instruction.  Two exchanges
+//   add the four slices and leave lane L with token L.
+//   Values: a lane takes 8 or 16 dimensions (at d = 128 half a warp per token,
+//   two tokens at a time), the weights broadcast.
 //
-// Bound: issue slots.  Per token, 4 dimensions and RG = 8 rows the score
-// loop issues about 34 instructions (16 f32x2, 12 shared-memory loads), the
-// value loop as many.
+// Bound: shared-memory loads (a lookup per code and lane, weights and queries)
+// and the FMA pipe, about 10 and 8 cycles of an SM per token, KV head and 8
+// rows at d = 128.
 
 constexpr int kAnyWarps = 4;
 constexpr int kAnyThreads = 32 * kAnyWarps;
@@ -30,10 +32,14 @@ struct AnyCfg {
   static constexpr int PB = D * BITS / 8;
   static constexpr int RS = ((PB / 16) | 1) * 16;           // row stride in shared memory
   static constexpr int STAGE = 2 * 32 * RS;                 // K rows, V rows of a block
-  static constexpr int OFF_Q = 2 * kAnyWarps * STAGE;       // [D][RG] rotated queries
-  static constexpr int OFF_W = OFF_Q + D * RG * 4;          // [warp][32][RG] weights
-  static constexpr int OFF_TAB = OFF_W + kAnyWarps * 32 * RG * 4;   // [16] (c, c)
-  static constexpr int OFF_ML = OFF_TAB + 16 * 8;           // [warp][RG] (m, l)
+  // Rotated queries [32-code group][dim][RG], 8 floats between groups: the
+  // four groups that a warp reads at once lie in different banks.
+  static constexpr int Q_GROUP = 32 * RG + 8;
+  static constexpr int OFF_Q = 2 * kAnyWarps * STAGE;
+  static constexpr int OFF_W = OFF_Q + (D / 32) * Q_GROUP * 4;      // [warp][32][RG] weights
+  static constexpr int OFF_TAB = OFF_W + kAnyWarps * 32 * RG * 4;   // [16] centroids
+  static constexpr int OFF_ML = OFF_TAB + 16 * 4;           // [warp][RG] (m, l)
+  static constexpr int PVL = D == 128 ? 16 : 32;            // lanes per token in the value loop
   static constexpr int SMEM = OFF_ML + kAnyWarps * RG * 8;
   static_assert(kAnyWarps * RG * D * 4 <= OFF_Q, "the warps' accumulators fit the stages");
 };
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(128) prep_rotate_kernel(const SplitArgs a) {
 template <int D, int BITS, int RG>
 __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs a) {
   using C = AnyCfg<D, BITS, RG>;
-  constexpr int PB = C::PB, RS = C::RS, KD = D / 32, RP = RG / 2;
+  constexpr int PB = C::PB, RS = C::RS, PVL = C::PVL, KD = D / PVL, RP = RG / 2;
   extern __shared__ __align__(128) unsigned char smem[];
   float *qs = reinterpret_cast<float *>(smem + C::OFF_Q);
   unsigned char *tab = smem + C::OFF_TAB;
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
   if (split >= (grp.prefix ? a.n_splits_p : a.n_splits)) return;
   const uint8_t *pk = grp.prefix ? a.prefix_k : a.packed_k, *pv = grp.prefix ? a.prefix_v : a.packed_v;
   const uint16_t *nk = grp.prefix ? a.prefix_nk : a.norms_k, *nv = grp.prefix ? a.prefix_nv : a.norms_v;
-  if (tid < 16) *reinterpret_cast<float2 *>(tab + 8 * tid) = make_float2(a.centroid[tid], a.centroid[tid]);
+  if (tid < 16) *reinterpret_cast<float *>(tab + 4 * tid) = a.centroid[tid];
 
   const long long tmax = grp.prefix ? a.prefix_max : a.tmax;
   int tlen = grp.prefix ? *a.prefix_len : a.seq_lens[row];
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
   pdl_launch_dependents();
   for (int i = tid; i < RG * D; i += kAnyThreads) {
     const int h = i / D, e = i % D;
-    qs[e * RG + h] = h < rows ? a.ws_qrot[group_query(a, grp, kvh, h) * D + e] : 0.f;
+    qs[(e >> 5) * C::Q_GROUP + (e & 31) * RG + h] = h < rows ? a.ws_qrot[group_query(a, grp, kvh, h) * D + e] : 0.f;
   }
   __syncthreads();
 
@@ -210,43 +216,78 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
     const unsigned mask = seen_mask(seen, block);
     const bool ok = (mask >> lane) & 1u;
 
-    // ---- scores: this lane's token against the query rows ----
-    uint64_t dot[RP];
+    // ---- scores: four tokens and a quarter of the dimensions per lane ----
+    uint64_t dot[4][RP];
 #pragma unroll
-    for (int r = 0; r < RP; ++r) dot[r] = 0ull;
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < RP; ++r) dot[i][r] = 0ull;
+    const int tl = lane & 7, sl = lane >> 3;
 #pragma unroll 1
     for (int seg = 0; seg < D / 128; ++seg) {
-      constexpr int W = 4 * BITS;   // words of 128 codes
-      uint32_t w[W];
+      const int grp32 = 4 * seg + sl;                 // this lane's 32-code group
+      uint32_t w[4][BITS];
 #pragma unroll
-      for (int p = 0; p < BITS; ++p) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(kc + lane * RS + seg * (16 * BITS) + 16 * p);
-        w[4 * p] = u.x;
-        w[4 * p + 1] = u.y;
-        w[4 * p + 2] = u.z;
-        w[4 * p + 3] = u.w;
+      for (int i = 0; i < 4; ++i) {
+        const unsigned char *src = kc + (tl + 8 * i) * RS + grp32 * (4 * BITS);
+        if constexpr (BITS == 4) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(src);
+          w[i][0] = u.x;
+          w[i][1] = u.y;
+          w[i][2] = u.z;
+          w[i][3] = u.w;
+        } else if constexpr (BITS == 2) {
+          const uint2 u = *reinterpret_cast<const uint2 *>(src);
+          w[i][0] = u.x;
+          w[i][1] = u.y;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 3; ++k) w[i][k] = *reinterpret_cast<const uint32_t *>(src + 4 * k);
+        }
       }
-      const float *qd = qs + seg * 128 * RG;
+      const float *qd = qs + grp32 * C::Q_GROUP;
 #pragma unroll
-      for (int quad = 0; quad < 32; ++quad) {
-        const uint32_t f = quad_fields<BITS>(w, quad);
+      for (int quad = 0; quad < 8; ++quad) {
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = quad_fields<BITS>(w[i], quad);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t off = e == 0 ? (f << 3) & 0x78u : (f >> (4 * e - 3)) & 0x78u;
-          const uint64_t c = *reinterpret_cast<const uint64_t *>(tab + off);
           const float *qe = qd + (4 * quad + e) * RG;
+          uint64_t qv[RP];
           if constexpr (RG >= 4) {
 #pragma unroll
             for (int r = 0; r < RG / 4; ++r) {
-              const ulonglong2 qv = *reinterpret_cast<const ulonglong2 *>(qe + 4 * r);
-              dot[2 * r] = f2_fma(c, qv.x, dot[2 * r]);
-              dot[2 * r + 1] = f2_fma(c, qv.y, dot[2 * r + 1]);
+              const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(qe + 4 * r);
+              qv[2 * r] = u.x;
+              qv[2 * r + 1] = u.y;
             }
           } else {
-            dot[0] = f2_fma(c, *reinterpret_cast<const uint64_t *>(qe), dot[0]);
+            qv[0] = *reinterpret_cast<const uint64_t *>(qe);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float c = *reinterpret_cast<const float *>(tab + (e == 0 ? (f[i] << 2) & 0x3Cu : (f[i] >> (4 * e - 2)) & 0x3Cu));
+            const uint64_t c2 = f2_pack(c, c);
+#pragma unroll
+            for (int r = 0; r < RP; ++r) dot[i][r] = f2_fma(c2, qv[r], dot[i][r]);
           }
         }
       }
+    }
+    // Add the four slices: lanes s and s ^ 2 share tokens (0, 1) and (2, 3),
+    // then s and s ^ 1 one each; lane L = t + 8 s is left with token L.
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        const uint64_t give = (sl & 2) ? dot[i][r] : dot[i + 2][r], keep = (sl & 2) ? dot[i + 2][r] : dot[i][r];
+        dot[i][r] = f2_add(keep, __shfl_xor_sync(0xffffffffu, give, 16));
+      }
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      const uint64_t give = (sl & 1) ? dot[0][r] : dot[1][r], keep = (sl & 1) ? dot[1][r] : dot[0][r];
+      dot[0][r] = f2_add(keep, __shfl_xor_sync(0xffffffffu, give, 8));
     }
     // ---- softmax (log2 domain); the reference maximum moves only when a
     // score passes it by 8, so p <= 2^8 ----
@@ -254,7 +295,7 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
     bool over = false;
 #pragma unroll
     for (int r = 0; r < RP; ++r) {
-      f2_unpack(dot[r], x[2 * r], x[2 * r + 1]);
+      f2_unpack(dot[0][r], x[2 * r], x[2 * r + 1]);
       x[2 * r] = ok ? x[2 * r] * sk : -INFINITY;
       x[2 * r + 1] = ok ? x[2 * r + 1] * sk : -INFINITY;
       over |= x[2 * r] > m[2 * r] + 8.f || x[2 * r + 1] > m[2 * r + 1] + 8.f;
@@ -289,9 +330,14 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
     for (int r = 0; r < RP; ++r) *reinterpret_cast<float2 *>(wts + lane * RG + 2 * r) = make_float2(x[2 * r], x[2 * r + 1]);
     __syncwarp();
 
-    // ---- values: this lane's dimensions over the block's seen tokens ----
-    for (unsigned left = mask; left; left &= left - 1) {
-      const int j = __ffs(left) - 1;
+    // ---- values: this lane's dimensions over the block's tokens; a token that
+    // is not seen has weight 0 (and codes of whatever the stage held) ----
+    constexpr int TPW = 32 / PVL;                    // tokens at a time
+    const int th = lane / PVL, vl = lane % PVL;
+    const int n_tok = 32 - __clz(mask);              // past the last token seen
+#pragma unroll 2
+    for (int j0 = 0; j0 < n_tok; j0 += TPW) {
+      const int j = j0 + th;
       uint64_t w2[RP];
       if constexpr (RG >= 4) {
 #pragma unroll
@@ -306,13 +352,13 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
       const uint32_t *vr = reinterpret_cast<const uint32_t *>(vc + j * RS);
 #pragma unroll
       for (int u = 0; u < KD / 4; ++u) {
-        const uint32_t f = quad_fields<BITS>(vr, (KD / 4) * lane + u);
+        const uint32_t f = quad_fields<BITS>(vr, (KD / 4) * vl + u);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t off = e == 0 ? (f << 3) & 0x78u : (f >> (4 * e - 3)) & 0x78u;
-          const uint64_t c = *reinterpret_cast<const uint64_t *>(tab + off);
+          const float c = *reinterpret_cast<const float *>(tab + (e == 0 ? (f << 2) & 0x3Cu : (f >> (4 * e - 2)) & 0x3Cu));
+          const uint64_t c2 = f2_pack(c, c);
 #pragma unroll
-          for (int r = 0; r < RP; ++r) acc[4 * u + e][r] = f2_fma(c, w2[r], acc[4 * u + e][r]);
+          for (int r = 0; r < RP; ++r) acc[4 * u + e][r] = f2_fma(c2, w2[r], acc[4 * u + e][r]);
         }
       }
     }
@@ -327,6 +373,12 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
     for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
     if (lane == 0) ml[warp * RG + r] = make_float2(m[r], l[r]);
   }
+  if constexpr (PVL == 16) {   // the two half warps' tokens
+#pragma unroll
+    for (int k = 0; k < KD; ++k)
+#pragma unroll
+      for (int r = 0; r < RP; ++r) acc[k][r] = f2_add(acc[k][r], __shfl_xor_sync(0xffffffffu, acc[k][r], 16));
+  }
   __syncthreads();   // every warp is done with its stages
   float *sl = reinterpret_cast<float *>(smem);   // [warp][RG][D]
 #pragma unroll
@@ -335,8 +387,10 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
     for (int k = 0; k < KD; ++k) {
       float u0, u1;
       f2_unpack(acc[k][r], u0, u1);
-      sl[(warp * RG + 2 * r) * D + KD * lane + k] = u0;
-      sl[(warp * RG + 2 * r + 1) * D + KD * lane + k] = u1;
+      if (PVL == 32 || lane < 16) {
+        sl[(warp * RG + 2 * r) * D + KD * (lane % PVL) + k] = u0;
+        sl[(warp * RG + 2 * r + 1) * D + KD * (lane % PVL) + k] = u1;
+      }
     }
   }
   __syncthreads();
