@@ -563,50 +563,31 @@ def _fits(q, pk, pv, nk, nv, lens, prk, prv, hkv, d, bits, batch) -> bool:
             prk.is_contiguous() and prv.is_contiguous())
 
 
-def _out_of(out, q):
-    if out is None:
-        return _torch().empty_like(q)
+def _given_out(out, q):
     if out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, with the shape and dtype of q")
     if out.device != q.device:
         raise ValueError("all tensors must be on the same device")
-    return out
-
-
-class _on:
-    """The device made current for a launch, where it is not already."""
-
-    def __init__(self, index):
-        cuda = _torch().cuda
-        self.guard = None if cuda.current_device() == index else cuda.device(index)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _raw_stream(index: int, stream) -> int:
-    if stream is None:
-        return _torch()._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _scratch(workspace, nbytes, dev):
-    """The caller's workspace, or one from torch's allocator; and its bytes."""
-    if workspace is None:
-        t = _torch()
-        return t.empty(nbytes, dtype=t.uint8, device=dev), nbytes
-    if not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError("workspace must be contiguous and on the device of q")
-    return workspace, workspace.numel() * workspace.element_size()
+    """Address and bytes of the caller's workspace, or of one from torch's
+    allocator (returned too: it lives until the launch is queued)."""
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError("workspace must be contiguous and on the device of q")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if nbytes == 0:
+        return None, None, 0
+    t = _torch()
+    workspace = t.empty(nbytes, dtype=t.uint8, device=dev)
+    return workspace, workspace.data_ptr(), nbytes
 
 
-def _scale(scale: Optional[float], d: int) -> float:
-    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+def _elsewhere(call, index, *args, **kwargs):
+    """The call with its tensors' device made current."""
+    with _torch().cuda.device(index):
+        return call(*args, **kwargs)
 
 
 @functools.lru_cache(maxsize=256)
@@ -633,15 +614,20 @@ def isoq_decode_attention_window(q, packed_k, packed_v, norms_k, norms_v, seq_le
         _cache_refusal(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B,
                        [(batch == B, "q and the cache differ in their batch")],
                        (q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v))
-    with _on(index):
-        out = _out_of(out, q)
-        workspace, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink),
-                                 q.device)
-        st = lib().isoq_decode_attention_window(
-            q.data_ptr(), _dtype_code(q), packed_k.data_ptr(), packed_v.data_ptr(), norms_k.data_ptr(),
-            norms_v.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, Tmax, d, bits, variant, params_k.data_ptr(),
-            params_v.data_ptr(), _scale(scale, d), window, n_sink, out.data_ptr(), workspace.data_ptr(), ws,
-            _raw_stream(index, stream))
+    t = _torch()
+    if t.cuda.current_device() != index:
+        return _elsewhere(isoq_decode_attention_window, index, q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k,
+                          params_v, bits, variant, window, n_sink, scale, out, workspace, stream)
+    if out is None:
+        out = t.empty_like(q)
+    else:
+        _given_out(out, q)
+    workspace, wp, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink), q.device)
+    st = lib().isoq_decode_attention_window(
+        q.data_ptr(), _dtype_code(q), packed_k.data_ptr(), packed_v.data_ptr(), norms_k.data_ptr(), norms_v.data_ptr(),
+        seq_lens.data_ptr(), B, Hq, Hkv, Tmax, d, bits, variant, params_k.data_ptr(), params_v.data_ptr(),
+        d ** -0.5 if scale is None else scale, window, n_sink, out.data_ptr(), wp, ws,
+        t._C._cuda_getCurrentRawStream(index) if stream is None else _stream(None, stream))
     if st:
         _check(st, "isoq_decode_attention_window")
     return out
@@ -662,12 +648,19 @@ def isoq_prefill_attention_window(q, packed_k, packed_v, norms_k, norms_v, seq_l
         _cache_refusal(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B,
                        [(batch == B, "q and the cache differ in their batch")],
                        (q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v))
-    with _on(index):
-        out = _out_of(out, q)
-        st = lib().isoq_prefill_attention_window(
-            q.data_ptr(), _dtype_code(q), packed_k.data_ptr(), packed_v.data_ptr(), norms_k.data_ptr(),
-            norms_v.data_ptr(), seq_lens.data_ptr(), B, Tq, Hq, Hkv, Tmax, d, bits, variant, params_k.data_ptr(),
-            params_v.data_ptr(), _scale(scale, d), window, n_sink, out.data_ptr(), _raw_stream(index, stream))
+    t = _torch()
+    if t.cuda.current_device() != index:
+        return _elsewhere(isoq_prefill_attention_window, index, q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k,
+                          params_v, bits, variant, window, n_sink, scale, out, stream)
+    if out is None:
+        out = t.empty_like(q)
+    else:
+        _given_out(out, q)
+    st = lib().isoq_prefill_attention_window(
+        q.data_ptr(), _dtype_code(q), packed_k.data_ptr(), packed_v.data_ptr(), norms_k.data_ptr(), norms_v.data_ptr(),
+        seq_lens.data_ptr(), B, Tq, Hq, Hkv, Tmax, d, bits, variant, params_k.data_ptr(), params_v.data_ptr(),
+        d ** -0.5 if scale is None else scale, window, n_sink, out.data_ptr(),
+        t._C._cuda_getCurrentRawStream(index) if stream is None else _stream(None, stream))
     if st:
         _check(st, "isoq_prefill_attention_window")
     return out
@@ -708,15 +701,21 @@ def isoq_decode_attention_prefix(q, prefix_k, prefix_v, prefix_norms_k, prefix_n
                         (prefix_len.dtype is t.int32 and prefix_len.numel() == 1, "prefix_len is one int32")],
                        (q, prefix_k, prefix_v, prefix_norms_k, prefix_norms_v, prefix_len, packed_k, packed_v, norms_k,
                         norms_v, seq_lens, params_k, params_v))
-    with _on(index):
-        out = _out_of(out, q)
-        workspace, ws = _scratch(workspace, isoq_decode_prefix_workspace_size(B, Hq, Hkv, Tp, Tmax, d), q.device)
-        st = lib().isoq_decode_attention_prefix(
-            q.data_ptr(), _dtype_code(q), prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_norms_k.data_ptr(),
-            prefix_norms_v.data_ptr(), prefix_len.data_ptr(), Tp, apart, packed_k.data_ptr(), packed_v.data_ptr(),
-            norms_k.data_ptr(), norms_v.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, Tmax, d, bits, variant,
-            params_k.data_ptr(), params_v.data_ptr(), _scale(scale, d), out.data_ptr(), workspace.data_ptr(), ws,
-            _raw_stream(index, stream))
+    if t.cuda.current_device() != index:
+        return _elsewhere(isoq_decode_attention_prefix, index, q, prefix_k, prefix_v, prefix_norms_k, prefix_norms_v,
+                          prefix_len, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, bits, variant,
+                          scale, out, workspace, stream)
+    if out is None:
+        out = t.empty_like(q)
+    else:
+        _given_out(out, q)
+    workspace, wp, ws = _scratch(workspace, isoq_decode_prefix_workspace_size(B, Hq, Hkv, Tp, Tmax, d), q.device)
+    st = lib().isoq_decode_attention_prefix(
+        q.data_ptr(), _dtype_code(q), prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_norms_k.data_ptr(),
+        prefix_norms_v.data_ptr(), prefix_len.data_ptr(), Tp, apart, packed_k.data_ptr(), packed_v.data_ptr(),
+        norms_k.data_ptr(), norms_v.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, Tmax, d, bits, variant,
+        params_k.data_ptr(), params_v.data_ptr(), d ** -0.5 if scale is None else scale, out.data_ptr(), wp, ws,
+        t._C._cuda_getCurrentRawStream(index) if stream is None else _stream(None, stream))
     if st:
         _check(st, "isoq_decode_attention_prefix")
     return out
@@ -756,20 +755,25 @@ def isoq_build_block_tables(seq_lens, new_lens, free_pages, block_table, page_to
                  (total_lens is None or total_lens.numel() == B, f"total_lens does not have {B} entries"),
                  (pages_used is None or pages_used.numel() == 1, "pages_used is one int32"),
                  (n_slots in (None, slots), "slot_map does not have n_slots entries")], (*every, slot_map))
-    with _on(index):
-        dev = block_table.device
-        if slot_map is None:
-            slot_map = t.empty(slots, dtype=t.int64, device=dev)
-        if row_start is None:
-            row_start = t.empty(B + 1, dtype=t.int32, device=dev)
-        if total_lens is None:
-            total_lens = t.empty(B, dtype=t.int32, device=dev)
-        if pages_used is None:
-            pages_used = t.empty(1, dtype=t.int32, device=dev)
-        st = lib().isoq_build_block_tables(
-            seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), _ptr(free_head), free_pages.numel(), B,
-            page_tokens, max_pages, block_table.data_ptr(), slots, slot_map.data_ptr(), row_start.data_ptr(),
-            total_lens.data_ptr(), pages_used.data_ptr(), _raw_stream(index, stream))
+    if t.cuda.current_device() != index:
+        return _elsewhere(isoq_build_block_tables, index, seq_lens, new_lens, free_pages, block_table, page_tokens, n_slots,
+                          free_head, slot_map, row_start, total_lens, pages_used, stream)
+    dev = block_table.device
+    if slot_map is None:
+        slot_map = t.empty(slots, dtype=t.int64, device=dev)
+    if row_start is None and total_lens is None and pages_used is None:   # one allocation
+        row_start, total_lens, pages_used = t.empty(2 * B + 2, dtype=t.int32, device=dev).split((B + 1, B, 1))
+    if row_start is None:
+        row_start = t.empty(B + 1, dtype=t.int32, device=dev)
+    if total_lens is None:
+        total_lens = t.empty(B, dtype=t.int32, device=dev)
+    if pages_used is None:
+        pages_used = t.empty(1, dtype=t.int32, device=dev)
+    st = lib().isoq_build_block_tables(
+        seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), _ptr(free_head), free_pages.numel(), B,
+        page_tokens, max_pages, block_table.data_ptr(), slots, slot_map.data_ptr(), row_start.data_ptr(),
+        total_lens.data_ptr(), pages_used.data_ptr(),
+        t._C._cuda_getCurrentRawStream(index) if stream is None else _stream(None, stream))
     if st:
         _check(st, "isoq_build_block_tables")
     return slot_map, row_start, total_lens, pages_used
@@ -803,11 +807,13 @@ def isoq_paged_append(k_new, v_new, pages_k, pages_v, norms_k, norms_v, slot_map
                         (v_new.is_contiguous() and slot_map.is_contiguous(), "v_new and slot_map must be contiguous"),
                         (slot_map.numel() >= N, "slot_map has fewer entries than there are new tokens")],
                        (k_new, v_new, pages_k, pages_v, norms_k, norms_v, slot_map, params_k, params_v))
-    with _on(index):
-        st = lib().isoq_paged_append(
-            k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), pages_k.data_ptr(), pages_v.data_ptr(),
-            norms_k.data_ptr(), norms_v.data_ptr(), slot_map.data_ptr(), N, Hkv, n_pages, P, d, bits, variant,
-            params_k.data_ptr(), params_v.data_ptr(), _raw_stream(index, stream))
+    if t.cuda.current_device() != index:
+        return _elsewhere(isoq_paged_append, index, k_new, v_new, pages_k, pages_v, norms_k, norms_v, slot_map, params_k,
+                          params_v, bits, variant, stream)
+    st = lib().isoq_paged_append(
+        k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), pages_k.data_ptr(), pages_v.data_ptr(), norms_k.data_ptr(),
+        norms_v.data_ptr(), slot_map.data_ptr(), N, Hkv, n_pages, P, d, bits, variant, params_k.data_ptr(),
+        params_v.data_ptr(), t._C._cuda_getCurrentRawStream(index) if stream is None else _stream(None, stream))
     if st:
         _check(st, "isoq_paged_append")
 
@@ -837,15 +843,19 @@ def isoq_paged_decode_attention(q, pages_k, pages_v, norms_k, norms_v, block_tab
         max_len = max_pages * P
     if window is None:
         window = max_len
-    with _on(index):
-        out = _out_of(out, q)
-        workspace, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, max_len, d, window, n_sink),
-                                 q.device)
-        st = lib().isoq_paged_decode_attention(
-            q.data_ptr(), _dtype_code(q), pages_k.data_ptr(), pages_v.data_ptr(), norms_k.data_ptr(), norms_v.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, n_pages, P, max_pages, max_len, d, bits, variant,
-            params_k.data_ptr(), params_v.data_ptr(), _scale(scale, d), window, n_sink, out.data_ptr(),
-            workspace.data_ptr(), ws, _raw_stream(index, stream))
+    if t.cuda.current_device() != index:
+        return _elsewhere(isoq_paged_decode_attention, index, q, pages_k, pages_v, norms_k, norms_v, block_table, seq_lens,
+                          params_k, params_v, bits, variant, max_len, window, n_sink, scale, out, workspace, stream)
+    if out is None:
+        out = t.empty_like(q)
+    else:
+        _given_out(out, q)
+    workspace, wp, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, max_len, d, window, n_sink), q.device)
+    st = lib().isoq_paged_decode_attention(
+        q.data_ptr(), _dtype_code(q), pages_k.data_ptr(), pages_v.data_ptr(), norms_k.data_ptr(), norms_v.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, n_pages, P, max_pages, max_len, d, bits, variant,
+        params_k.data_ptr(), params_v.data_ptr(), d ** -0.5 if scale is None else scale, window, n_sink, out.data_ptr(), wp,
+        ws, t._C._cuda_getCurrentRawStream(index) if stream is None else _stream(None, stream))
     if st:
         _check(st, "isoq_paged_decode_attention")
     return out

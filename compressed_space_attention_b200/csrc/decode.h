@@ -49,6 +49,12 @@ struct SplitArgs {
   int page_shift, max_pages, n_pages;
   float *ws_qrot;          // rotated float32 queries [B][Hq][d] (the CUDA-core split)
   int mode;
+  // One launch for everything: a cluster holds the splits of a row group, each
+  // CTA prepares its own queries, and the cluster merges the partial states in
+  // its shared memory, rotates back and stores (no workspace).
+  bool fused, full, half_out;
+  const float *params_v;
+  void *out;
 };
 
 // A page index of a block table outside [0, n_pages), or a slot outside the

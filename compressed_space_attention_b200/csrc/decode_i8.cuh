@@ -256,43 +256,19 @@ __device__ __forceinline__ long long state_slot(const SplitArgs &a, const RowGro
   else return group_slot(a, g, kvh, h, split);
 }
 
-// Query preparation, one CTA per (b, kvh): rotate the G queries once,
-// q~ = R_K q, and write for every lane of the split kernel the B-fragment
-// words of the fixed-point query Q = rint(q~ / qinv) = 2^14 Qh + 2^7 Qm + Ql
-// (qinv = max|q~_h| / kQueryIntMax per head), then the per-head score factors
-// qinv_h * score_unit (0 for padded heads).  Word ((nq KK + kk) 2 + half) 32
-// + lane holds tile nq, k-step kk, half `half` of lane (g, t): column g is
-// (head, part) with part p of head h in tile 0, column p GP + h (GP <= 2);
-// tile 0, column 4p + h for p < 2 and tile 1, column h for p = 2 (GP = 4);
-// tile p, column h (GP = 8); the four int8 values are the dims of quad
-// 2 (kk mod 4) + half of lane t's 32-code group (D = 128: group t; D = 256:
-// group 2t + kk / 4).
-//
-// One warp per query head h (GP warps), lane j holding dims E j .. E j + E - 1
-// (E = d / 32) in registers: the Walsh-Hadamard stages h < E inside the
-// lane, the others by shuffles with lane j ^ (h / E), in the same stage
-// order and with the same sums as the shared-memory rotation (so q~ is the
-// same to the bit), then 1/sqrt(d) and the block map on the lane's own 4-dim
-// blocks.  The part words go through shared memory once to their fragment
-// positions.
-//
-// In the modes (SplitMode) other than kSplitDense blockIdx.y is a group of
-// query rows (RowGroup) instead of a batch row.
-template <int D, bool FULL, int GP, int MODE = kSplitDense>
-__global__ void __launch_bounds__(32 * GP) prep_i8_kernel(const SplitArgs a, float score_unit) {
-  using C = I8Cfg<D, GP>;
-  constexpr int E = D / 32, NQUAD = D / 4;
-  __shared__ uint32_t pw[3][GP][NQUAD];   // part p of head h, dims 4 quad .. + 3
-  __shared__ float qinv_s[8];
-  const int kvh = blockIdx.x, b = blockIdx.y;
-  const int tid = threadIdx.x, h = tid >> 5, lane = tid & 31;
-  const RowGroup grp_rows = cta_rows<MODE>(a, b);
-  const int G = grp_rows.rows;
-  pdl_launch_dependents();   // the split kernel may start its staging now
-
+// One head by one warp, lane j holding dims E j .. E j + E - 1 (E = d / 32): the
+// Walsh-Hadamard stages h < E inside the lane, the others by shuffles with
+// lane j ^ (h / E), in the same stage order and with the same sums as the
+// shared-memory rotation, then 1/sqrt(d) and the block map on the lane's own
+// 4-dim blocks.  Part p of the fixed-point query, quad by quad, at
+// parts + p part_stride; q = nullptr is a zero query.
+template <int D>
+__device__ __forceinline__ void prepare_head(const __half *q, const float *prm, bool full, int lane, uint32_t *parts,
+                                             int part_stride, float *qinv) {
+  constexpr int E = D / 32;
   float x[E];
-  if (h < G) {
-    const __half *qp = static_cast<const __half *>(a.q) + group_query(a, grp_rows, kvh, h) * D + E * lane;
+  if (q) {
+    const __half *qp = q + E * lane;
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(qp + e));
@@ -325,44 +301,97 @@ __global__ void __launch_bounds__(32 * GP) prep_i8_kernel(const SplitArgs a, flo
     }
   }
   const float inv = rsqrtf(static_cast<float>(D));
-  const float *prm = a.params_k + static_cast<size_t>(kvh) * 2 * D;
   float mx = 0.f;
 #pragma unroll
   for (int u = 0; u < E / 4; ++u) {
     const int bi = (E / 4) * lane + u;
     const Quat v{x[4 * u] * inv, x[4 * u + 1] * inv, x[4 * u + 2] * inv, x[4 * u + 3] * inv};
-    const Quat r = block_forward(load_quat(prm + 8 * bi), load_quat(prm + 8 * bi + 4), v, FULL);
+    const Quat r = block_forward(load_quat(prm + 8 * bi), load_quat(prm + 8 * bi + 4), v, full);
     x[4 * u] = r.w;
     x[4 * u + 1] = r.x;
     x[4 * u + 2] = r.y;
     x[4 * u + 3] = r.z;
   }
-  if (h < G) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
-  }
+  for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float qi = mx / static_cast<float>(kQueryIntMax);
   const float qsc = qi > 0.f ? 1.f / qi : 0.f;
-  if (lane == 0) qinv_s[h] = qi;
-  if (h == 0 && lane >= GP && lane < 8) qinv_s[lane] = 0.f;
+  if (lane == 0) *qinv = qi;
 #pragma unroll
   for (int u = 0; u < E / 4; ++u) {
     int v[3][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      int q = h < G ? __float2int_rn(x[4 * u + i] * qsc) : 0;
-      q = q > kQueryIntMax ? kQueryIntMax : (q < -kQueryIntMax ? -kQueryIntMax : q);
-      const int r1 = (q + 64) >> 7, ql = q - 128 * r1;     // arithmetic shifts: floor
+      int qi22 = __float2int_rn(x[4 * u + i] * qsc);
+      qi22 = qi22 > kQueryIntMax ? kQueryIntMax : (qi22 < -kQueryIntMax ? -kQueryIntMax : qi22);
+      const int r1 = (qi22 + 64) >> 7, ql = qi22 - 128 * r1;     // arithmetic shifts: floor
       const int r2 = (r1 + 64) >> 7, qm = r1 - 128 * r2;
       v[0][i] = r2;
       v[1][i] = qm;
       v[2][i] = ql;
     }
 #pragma unroll
-    for (int p = 0; p < 3; ++p) pw[p][h][(E / 4) * lane + u] = pack_s8x4(v[p][0], v[p][1], v[p][2], v[p][3]);
+    for (int p = 0; p < 3; ++p) parts[p * part_stride + (E / 4) * lane + u] = pack_s8x4(v[p][0], v[p][1], v[p][2], v[p][3]);
   }
+}
+
+// Where word (nq, kk, half) of lane `ln`'s B fragments comes from: part, head
+// and quad of the fixed-point query (part 3: none).
+template <int D, int GP>
+__device__ __forceinline__ void fragment_source(int nq, int kk, int half, int ln, int &part, int &head, int &quad) {
+  const int g = ln >> 2, t = ln & 3;
+  if constexpr (GP <= 2) {
+    part = g / GP;
+    head = g % GP;
+  } else if constexpr (GP == 4) {
+    part = nq == 0 ? (g >> 2) : (g < 4 ? 2 : 3);
+    head = g & 3;
+  } else {
+    part = nq;
+    head = g;
+  }
+  quad = 8 * ((D == 256 ? 2 * t : t) + kk / 4) + 2 * (kk & 3) + half;
+}
+
+// Query preparation, one CTA per (b, kvh): rotate the G queries once,
+// q~ = R_K q, and write for every lane of the split kernel the B-fragment
+// words of the fixed-point query Q = rint(q~ / qinv) = 2^14 Qh + 2^7 Qm + Ql
+// (qinv = max|q~_h| / kQueryIntMax per head), then the per-head score factors
+// qinv_h * score_unit (0 for padded heads).  Word ((nq KK + kk) 2 + half) 32
+// + lane holds tile nq, k-step kk, half `half` of lane (g, t): column g is
+// (head, part) with part p of head h in tile 0, column p GP + h (GP <= 2);
+// tile 0, column 4p + h for p < 2 and tile 1, column h for p = 2 (GP = 4);
+// tile p, column h (GP = 8); the four int8 values are the dims of quad
+// 2 (kk mod 4) + half of lane t's 32-code group (D = 128: group t; D = 256:
+// group 2t + kk / 4).
+//
+// One warp per query head h (GP warps), lane j holding dims E j .. E j + E - 1
+// (E = d / 32) in registers: the Walsh-Hadamard stages h < E inside the
+// lane, the others by shuffles with lane j ^ (h / E), in the same stage
+// order and with the same sums as the shared-memory rotation (so q~ is the
+// same to the bit), then 1/sqrt(d) and the block map on the lane's own 4-dim
+// blocks.  The part words go through shared memory once to their fragment
+// positions.
+//
+// In the modes (SplitMode) other than kSplitDense blockIdx.y is a group of
+// query rows (RowGroup) instead of a batch row.
+template <int D, bool FULL, int GP, int MODE = kSplitDense>
+__global__ void __launch_bounds__(32 * GP) prep_i8_kernel(const SplitArgs a, float score_unit) {
+  using C = I8Cfg<D, GP>;
+  constexpr int NQUAD = D / 4;
+  __shared__ uint32_t pw[3][GP][NQUAD];   // part p of head h, dims 4 quad .. + 3
+  __shared__ float qinv_s[8];
+  const int kvh = blockIdx.x, b = blockIdx.y;
+  const int tid = threadIdx.x, h = tid >> 5, lane = tid & 31;
+  const RowGroup grp_rows = cta_rows<MODE>(a, b);
+  const int G = grp_rows.rows;
+  pdl_launch_dependents();   // the split kernel may start its staging now
+
+  prepare_head<D>(h < G ? static_cast<const __half *>(a.q) + group_query(a, grp_rows, kvh, h) * D : nullptr,
+                  a.params_k + static_cast<size_t>(kvh) * 2 * D, FULL, lane, &pw[0][h][0], GP * NQUAD, &qinv_s[h]);
+  if (h == 0 && lane >= GP && lane < 8) qinv_s[lane] = 0.f;
   __syncthreads();
 
   // Word ((nq KK + kk) 2 + half) 32 + lane of the B fragments (see above).
@@ -370,21 +399,9 @@ __global__ void __launch_bounds__(32 * GP) prep_i8_kernel(const SplitArgs a, flo
   constexpr int NWORDS = C::NQ * C::KK * 2 * 32;
   for (int idx = tid; idx < NWORDS; idx += 32 * GP) {
     const int ln = idx & 31, half = (idx >> 5) & 1, kk = (idx >> 6) % C::KK, nq = (idx >> 6) / C::KK;
-    const int g = ln >> 2, t = ln & 3;
-    int head, part;
-    if constexpr (GP <= 2) {
-      part = g / GP;
-      head = g % GP;
-    } else if constexpr (GP == 4) {
-      part = nq == 0 ? (g >> 2) : (g < 4 ? 2 : 3);
-      head = g & 3;
-    } else {
-      part = nq;
-      head = g;
-    }
-    const bool live = part < 3 && head < G;
-    const int grp = (D == 256 ? 2 * t : t) + kk / 4;
-    out[idx] = live ? pw[part][head][8 * grp + 2 * (kk & 3) + half] : 0u;
+    int head, part, quad;
+    fragment_source<D, GP>(nq, kk, half, ln, part, head, quad);
+    out[idx] = part < 3 && head < G ? pw[part][head][quad] : 0u;
   }
   if (tid < 8) out[3 * C::KK * 2 * 32 + tid] = __float_as_uint(tid < G ? qinv_s[tid] * score_unit : 0.f);
 }
@@ -580,10 +597,39 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
   // prepared once per (b, kvh) by prep_i8_kernel (launched just before this
   // kernel with programmatic dependent launch: wait for it here, after the
   // staging above has started).
+  constexpr bool CAN_FUSE = SLICES && (MODE == kSplitWindow || MODE == kSplitPaged);
+  __shared__ float2 fused_ml[CAN_FUSE ? 8 : 1];   // first the queries' steps, at the end (m, l)
+  const bool fused = CAN_FUSE && a.fused;
+  uint32_t qb[C::NQ][C::KK][2];
+  float qk0, qk1;
+  if (fused) {
+    // This CTA's own preparation (the cluster has no earlier launch), its
+    // parts in the merge scratch.
+    constexpr int NQUAD = D / 4;
+    uint32_t *pw = reinterpret_cast<uint32_t *>(scratch);   // [3][GP][NQUAD], below GP D floats
+#pragma unroll
+    for (int h = warp; h < GP; h += kI8Warps)
+      prepare_head<D>(h < G ? static_cast<const __half *>(a.q) + group_query(a, grp_rows, kvh, h) * D : nullptr,
+                      a.params_k + static_cast<size_t>(kvh) * 2 * D, a.full, lane, pw + h * NQUAD, GP * NQUAD, &fused_ml[h].x);
+    if (tid >= GP && tid < 8) fused_ml[tid].x = 0.f;
+    __syncthreads();
+#pragma unroll
+    for (int nq = 0; nq < C::NQ; ++nq)
+#pragma unroll
+      for (int kk = 0; kk < C::KK; ++kk)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          int part, head, quad;
+          fragment_source<D, GP>(nq, kk, half, lane, part, head, quad);
+          qb[nq][kk][half] = part < 3 && head < G ? pw[(part * GP + head) * NQUAD + quad] : 0u;
+        }
+    const float unit = a.scale * out_scale * 1.4426950408889634f;
+    qk0 = fused_ml[C::COMPACT ? 0 : 2 * t].x * unit;
+    qk1 = fused_ml[C::COMPACT ? 1 : 2 * t + 1].x * unit;
+  } else {
   pdl_launch_dependents();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t *qp = a.ws_qprep + pair * C::QPREP_WORDS;
-  uint32_t qb[C::NQ][C::KK][2];
 #pragma unroll
   for (int nq = 0; nq < C::NQ; ++nq)
 #pragma unroll
@@ -592,8 +638,9 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
       for (int half = 0; half < 2; ++half) qb[nq][kk][half] = qp[((nq * C::KK + kk) * 2 + half) * 32 + lane];
   // score factors of the lane's two heads: 2t, 2t + 1, or with the compact
   // softmax (GP <= 2) heads 0, 1 in every lane; 0 for padded heads
-  const float qk0 = __uint_as_float(qp[3 * C::KK * 2 * 32 + (C::COMPACT ? 0 : 2 * t)]);
-  const float qk1 = __uint_as_float(qp[3 * C::KK * 2 * 32 + (C::COMPACT ? 1 : 2 * t + 1)]);
+  qk0 = __uint_as_float(qp[3 * C::KK * 2 * 32 + (C::COMPACT ? 0 : 2 * t)]);
+  qk1 = __uint_as_float(qp[3 * C::KK * 2 * 32 + (C::COMPACT ? 1 : 2 * t + 1)]);
+  }
 
   // prmt selectors that move byte k of a packed (W_a, W_b) word to byte g&3
   // of a PV B register (zeros elsewhere): lo / hi byte of head parity g>>2.
@@ -1079,8 +1126,8 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
         const float mw = wm[w2 * 8 + h];
         f[w2] = mw == -INFINITY ? 0.f : exp2f(mw - mstar);
       }
-      const long long slot = state_slot<MODE>(a, grp_rows, kvh, h, split);
-      float *acc_out = a.ws_acc + slot * D;
+      const long long slot = fused ? 0 : state_slot<MODE>(a, grp_rows, kvh, h, split);
+      float *acc_out = fused ? scratch + h * D : a.ws_acc + slot * D;
       for (int i = tid; i < D; i += kI8Threads) {
         float sum = 0.f;
   #pragma unroll
@@ -1090,8 +1137,14 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
       if (tid == 0) {
         float l = 0.f;
         for (int w2 = 0; w2 < kI8Warps; ++w2) l += wl[w2 * 8 + h] * f[w2];
-        a.ws_ml[slot] = make_float2(mstar == -INFINITY ? -INFINITY : mstar * 0.69314718055994531f, l);
+        if (fused)
+          fused_ml[h] = make_float2(mstar, l);   // log2 domain
+        else
+          a.ws_ml[slot] = make_float2(mstar == -INFINITY ? -INFINITY : mstar * 0.69314718055994531f, l);
       }
+    }
+    if constexpr (CAN_FUSE) {
+      if (fused) cluster_finish<D>(a, grp_rows, kvh, scratch, fused_ml, warp, lane, kI8Warps);
     }
   } else {
     __syncthreads();   // all warps are done with the q~ scratch
@@ -1236,6 +1289,11 @@ int launch_split_i8(const SplitArgs &a, cudaStream_t stream) {
   const int z = MODE == kSplitDense ? a.batch : group_count(a, MODE);
   dim3 grid(MODE == kSplitPrefix && a.n_splits_p > a.n_splits ? a.n_splits_p : a.n_splits, a.hkv, z);
   static_assert(C::QPREP_WORDS == decode_qprep_words(D), "prepared-query layout");
+  if (MODE != kSplitDense && a.fused) {
+    cudaError_t e = launch_cluster(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a, tb.lut, out_scale);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "decode i8 cluster launch: %s", cudaGetErrorString(e));
+  }
   prep_i8_kernel<D, FULL, GP, MODE><<<dim3(a.hkv, z), 32 * GP, 0, stream>>>(a, score_unit);
   cudaError_t e = launch_pdl(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a, tb.lut, out_scale);
   if (e == cudaSuccess) e = cudaGetLastError();

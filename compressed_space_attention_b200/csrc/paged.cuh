@@ -18,7 +18,7 @@
 
 constexpr int kTableThreads = 256;
 constexpr int kTableRows = 1024;     // requests per pass
-constexpr int kTableTokens = 2048;   // slots per CTA
+constexpr int kTableTokens = 512;    // slots per CTA, two per thread at once
 
 struct TableArgs {
   const int32_t *seq_lens, *new_lens, *free_pages, *free_head;
@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(const Table
 
     // This CTA's slots of these requests.
     const long long f0 = start_s[0] > lo ? start_s[0] : lo, f1 = start_s[nb] < hi ? start_s[nb] : hi;
+#pragma unroll 2
     for (long long i = f0 + tid; i < f1; i += kTableThreads) {
       int x = 0, y = nb;   // the last request with start <= i
       while (y - x > 1) {
@@ -450,10 +451,11 @@ __global__ void __launch_bounds__(128) paged_append_kernel(const PagedAppendArgs
 
 template <typename T, int D, int BITS>
 int launch_paged_append(int variant, const PagedAppendArgs &a, cudaStream_t st) {
-  // Up to about 8 CTAs per SM over all heads; a warp walks the rest.
+  // The CTAs that are resident at once (4 per SM) over all heads; a warp walks
+  // the rest.
   constexpr int VPC = 4 * (512 / D);   // tokens of a CTA per turn
   const long long turns = (a.n_tok + VPC - 1) / VPC;
-  long long gx = (8 * 148 + 2 * a.hkv - 1) / (2 * a.hkv);
+  long long gx = (4 * 148 + 2 * a.hkv - 1) / (2 * a.hkv);
   if (gx > turns) gx = turns;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(2 * a.hkv));
   if (variant == ISOQ_FULL)

@@ -70,21 +70,13 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rotated queries q~ = R_K q scale log2(e), one warp per query row: the
-// Walsh-Hadamard stages h < E inside the lane, the others by shuffles, then
-// 1 / sqrt(d) and the block maps (the order of prep_i8_kernel).
-template <typename T, int D, bool FULL>
-__global__ void __launch_bounds__(128) prep_rotate_kernel(const SplitArgs a) {
+// q~ = R_K q scale log2(e) of one query row by one warp, lane j holding dims
+// E j .. E j + E - 1 (E = d / 32) before and after: the Walsh-Hadamard stages
+// h < E inside the lane, the others by shuffles, then 1 / sqrt(d) and the block
+// maps (the order of prep_i8_kernel).
+template <int D>
+__device__ __forceinline__ void rotate_query(float (&x)[D / 32], const float *prm, bool full, float scale, int lane) {
   constexpr int E = D / 32;
-  pdl_launch_dependents();
-  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (r >= static_cast<long long>(a.batch) * a.hq) return;
-  const int kvh = static_cast<int>(r % a.hq) / a.group;
-  const T *q = static_cast<const T *>(a.q) + r * D + E * lane;
-  float x[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = to_f32<T>(q[e]);
 #pragma unroll
   for (int hs = 1; hs < E; hs <<= 1) {
 #pragma unroll
@@ -106,16 +98,36 @@ __global__ void __launch_bounds__(128) prep_rotate_kernel(const SplitArgs a) {
     }
   }
   const float inv = rsqrtf(static_cast<float>(D));
-  const float sc = a.scale * 1.4426950408889634f;
-  const float *prm = a.params_k + static_cast<size_t>(kvh) * 2 * D;
-  float *out = a.ws_qrot + r * D + E * lane;
+  const float sc = scale * 1.4426950408889634f;
 #pragma unroll
   for (int u = 0; u < E / 4; ++u) {
     const int bi = (E / 4) * lane + u;
     const Quat v{x[4 * u] * inv, x[4 * u + 1] * inv, x[4 * u + 2] * inv, x[4 * u + 3] * inv};
-    const Quat y = block_forward(load_quat(prm + 8 * bi), load_quat(prm + 8 * bi + 4), v, FULL);
-    *reinterpret_cast<float4 *>(out + 4 * u) = make_float4(y.w * sc, y.x * sc, y.y * sc, y.z * sc);
+    const Quat y = block_forward(load_quat(prm + 8 * bi), load_quat(prm + 8 * bi + 4), v, full);
+    x[4 * u] = y.w * sc;
+    x[4 * u + 1] = y.x * sc;
+    x[4 * u + 2] = y.y * sc;
+    x[4 * u + 3] = y.z * sc;
   }
+}
+
+// The rotated queries of all rows, one warp per row.
+template <typename T, int D, bool FULL>
+__global__ void __launch_bounds__(128) prep_rotate_kernel(const SplitArgs a) {
+  constexpr int E = D / 32;
+  pdl_launch_dependents();
+  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= static_cast<long long>(a.batch) * a.hq) return;
+  const int kvh = static_cast<int>(r % a.hq) / a.group;
+  const T *q = static_cast<const T *>(a.q) + r * D + E * lane;
+  float x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = to_f32<T>(q[e]);
+  rotate_query<D>(x, a.params_k + static_cast<size_t>(kvh) * 2 * D, FULL, a.scale, lane);
+  float *out = a.ws_qrot + r * D + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; e += 4) *reinterpret_cast<float4 *>(out + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
 }
 
 template <int D, int BITS, int RG>
@@ -182,11 +194,33 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
   if (warp < n_blk) fetch(v0 + warp, 0);
   cp_async_commit();
 
+  __shared__ float2 fused_ml[8];
+  if (a.fused) {   // the cluster has no earlier launch: this CTA rotates its own rows
+    constexpr int E = D / 32;
+    for (int h = warp; h < RG; h += kAnyWarps) {
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = 0.f;
+      if (h < rows) {
+        const long long at = group_query(a, grp, kvh, h) * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          x[e] = a.half_out ? __half2float(static_cast<const __half *>(a.q)[at + e]) : static_cast<const float *>(a.q)[at + e];
+      }
+      rotate_query<D>(x, a.params_k + static_cast<size_t>(kvh) * 2 * D, a.full, a.scale, lane);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int dim = E * lane + e;
+        qs[(dim >> 5) * C::Q_GROUP + (dim & 31) * RG + h] = x[e];
+      }
+    }
+  } else {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the rotated queries
   pdl_launch_dependents();
   for (int i = tid; i < RG * D; i += kAnyThreads) {
     const int h = i / D, e = i % D;
     qs[(e >> 5) * C::Q_GROUP + (e & 31) * RG + h] = h < rows ? a.ws_qrot[group_query(a, grp, kvh, h) * D + e] : 0.f;
+  }
   }
   __syncthreads();
 
@@ -404,15 +438,19 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
       f[w] = u.x == -INFINITY ? 0.f : exp2f(u.x - mx);
       lt += u.y * f[w];
     }
-    const long long slot = group_slot(a, grp, kvh, h, split);
+    const long long slot = a.fused ? 0 : group_slot(a, grp, kvh, h, split);
+    float *acc_out = a.fused ? qs + h * D : a.ws_acc + slot * D;   // fused: over the queries
     for (int i = tid; i < D; i += kAnyThreads) {
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kAnyWarps; ++w) sum += sl[(w * RG + h) * D + i] * f[w];
-      a.ws_acc[slot * D + i] = sum;
+      acc_out[i] = sum;
     }
-    if (tid == 0) a.ws_ml[slot] = make_float2(mx == -INFINITY ? -INFINITY : mx * 0.69314718055994531f, lt);
+    if (a.fused) {
+      if (tid == 0) fused_ml[h] = make_float2(mx, lt);   // log2 domain
+    } else if (tid == 0) a.ws_ml[slot] = make_float2(mx == -INFINITY ? -INFINITY : mx * 0.69314718055994531f, lt);
   }
+  if (a.fused) cluster_finish<D>(a, grp, kvh, qs, fused_ml, warp, lane, kAnyWarps);
 }
 
 // ---------------------------------------------------------------------------
@@ -448,6 +486,11 @@ int launch_split_any(const SplitArgs &a, cudaStream_t st) {
   auto kernel = split_any_kernel<D, BITS, RG>;
   const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (c != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "split: %s", cudaGetErrorString(c));
+  if (a.fused) {
+    cudaError_t e = launch_cluster(kernel, dim3(a.n_splits, a.hkv, group_count(a, a.mode)), dim3(kAnyThreads), C::SMEM, st, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "split cluster launch: %s", cudaGetErrorString(e));
+  }
   const int nx = a.mode == kSplitPrefix && a.n_splits_p > a.n_splits ? a.n_splits_p : a.n_splits;
   cudaError_t e = launch_pdl(kernel, dim3(nx, a.hkv, group_count(a, a.mode)), dim3(kAnyThreads), C::SMEM, st, a);
   if (e == cudaSuccess) e = cudaGetLastError();

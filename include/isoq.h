@@ -353,7 +353,9 @@ int isoq_prefill_attention(const void *q_dev, int dtype, const uint8_t *packed_k
  * The other arguments and rules as isoq_decode_attention; B <= 16384.
  * Float16 queries with 3-bit codes, d in {128, 256}, Tmax % 8 == 0 and norms
  * aligned to 16 bytes take the integer tensor-core split, everything else a
- * float32 one.  isoq_decode_window_workspace_size returns 0 on invalid shapes.
+ * float32 one.  isoq_decode_window_workspace_size returns 0 on invalid shapes,
+ * and where no workspace is needed (it may then be NULL): short lists of seen
+ * tokens, whose splits a thread-block cluster merges within one launch.
  */
 size_t isoq_decode_window_workspace_size(int B, int Hq, int Hkv, int64_t Tmax, int d, int64_t window,
                                          int64_t n_sink);

@@ -144,6 +144,34 @@ def test_window_decode_on_outlier_kv(window, n_sink, prefill_kv):
     _check(got, ref, F16, q, cache[2], cache[3], 1 / np.sqrt(128))
 
 
+@pytest.mark.parametrize("dtype,d,bits,hq,hkv", [HEADS[i] for i in (0, 2, 4, 6, 8, 9, 11, 13, 16)])
+def test_window_and_paged_decode_in_many_splits(dtype, d, bits, hq, hkv):
+    """Lists of seen tokens too long for one cluster: the three launches, sinks
+    and window in different splits, rows much shorter than the longest."""
+    g = np.random.default_rng(d + bits + hq)
+    tmax, p = 6400, 64
+    lens = np.array([6400, 5011, 4097, 90, 0], np.int32)
+    b = len(lens)
+    cache = _cache(g, (b, hkv, tmax), d, bits)
+    par = _params(hkv, d, 0)
+    q = g.standard_normal((b, hq, d)).astype(dtype)
+    scale = 1 / np.sqrt(d)
+    n = b * (tmax // p)
+    table = g.permutation(n).astype(np.int32).reshape(b, -1)
+    pages = [np.empty((n, hkv, p, *c.shape[3:]), c.dtype) for c in cache]
+    for i, c in enumerate(cache):
+        for r in range(b):
+            pages[i][table[r]] = c[r].reshape(hkv, tmax // p, p, *c.shape[3:]).swapaxes(0, 1)
+    dev, dpages, dpar, dl = [_t(c) for c in cache], [_t(x) for x in pages], [_t(x) for x in par], _t(lens)
+    for window, n_sink in [(4300, 300), (6400, 0)]:
+        assert isoq.isoq_decode_window_workspace_size(b, hq, hkv, tmax, d, window, n_sink) > 0
+        ref = S.window_decode(q, *cache, lens, *par, bits, 0, scale, window, n_sink)
+        got = isoq.isoq_decode_attention_window(_t(q), *dev, dl, *dpar, bits, 0, window, n_sink)
+        _check(got, ref, dtype, q, cache[2], cache[3], scale)
+        paged = isoq.isoq_paged_decode_attention(_t(q), *dpages, _t(table), dl, *dpar, bits, 0, window=window, n_sink=n_sink)
+        _check(paged, ref, dtype, q, cache[2], cache[3], scale)
+
+
 @pytest.mark.parametrize("d,hq,hkv", [(128, 4, 4), (128, 8, 4), (128, 8, 2), (128, 16, 2), (256, 4, 4), (256, 16, 2)])
 def test_window_prefill(d, hq, hkv):
     """Chunks at the end of ragged rows (one longer than its row), windows that
@@ -501,15 +529,15 @@ def test_captured_and_replayed_on_other_streams():
 def test_outputs_and_workspaces_end_where_they_say():
     """Sentinels behind the output and the workspace stay."""
     g = np.random.default_rng(6)
-    d, hq, hkv, b, tmax = 128, 6, 2, 3, 300
+    d, hq, hkv, b, tmax = 128, 6, 2, 3, 9000
     cache = [_t(c) for c in _cache(g, (b, hkv, tmax), d, 4)]
     par = [_t(x) for x in _params(hkv, d, 0)]
     q = _t(g.standard_normal((b, hq, d)).astype(F32))
-    lens = _t(np.array([300, 2, 250], np.int32))
-    n = isoq.isoq_decode_window_workspace_size(b, hq, hkv, tmax, d, 99, 7)
+    lens = _t(np.array([9000, 2, 250], np.int32))
+    n = isoq.isoq_decode_window_workspace_size(b, hq, hkv, tmax, d, 8000, 7)
     ws = torch.full((n + 256,), 77, dtype=torch.uint8, device=DEV)
     out = torch.full((b + 1, hq, d), 5.0, device=DEV)
-    isoq.isoq_decode_attention_window(q, *cache, lens, *par, 4, 0, 99, 7, out=out[:b], workspace=ws[:n])
+    isoq.isoq_decode_attention_window(q, *cache, lens, *par, 4, 0, 8000, 7, out=out[:b], workspace=ws[:n])
     assert (ws[n:] == 77).all() and (out[b] == 5).all() and (out[:b] != 5).all()
     with pytest.raises(isoq.IsoqError, match="workspace too small"):
-        isoq.isoq_decode_attention_window(q, *cache, lens, *par, 4, 0, 99, 7, workspace=ws[:n - 256])
+        isoq.isoq_decode_attention_window(q, *cache, lens, *par, 4, 0, 8000, 7, workspace=ws[:n - 256])

@@ -19,7 +19,7 @@ D128 = dict(q=P, dtype=0, pk=P, pv=P, nk=P, nv=P, lens=P, B=2, Hq=8, Hkv=2, Tmax
 
 
 def _window(**kw):
-    a = {**D128, **kw}
+    a = {**D128, "window": 16384, "Tmax": 1 << 15, **kw}
     return isoq.lib().isoq_decode_attention_window(
         a["q"], a["dtype"], a["pk"], a["pv"], a["nk"], a["nv"], a["lens"], a["B"], a["Hq"], a["Hkv"], a["Tmax"], a["d"],
         a["bits"], a["variant"], a["prk"], a["prv"], a["scale"], a["window"], a["n_sink"], a["out"], a["ws"],
@@ -42,7 +42,7 @@ def _prefix(**kw):
 
 
 def _paged(**kw):
-    a = {**D128, "table": P, "n_pages": 64, "page": 16, "max_pages": 16, **kw}
+    a = {**D128, "window": 1 << 15, "Tmax": 1 << 15, "table": P, "n_pages": 64, "page": 16, "max_pages": 2048, **kw}
     return isoq.lib().isoq_paged_decode_attention(
         a["q"], a["dtype"], a["pk"], a["pv"], a["nk"], a["nv"], a["table"], a["lens"], a["B"], a["Hq"], a["Hkv"],
         a["n_pages"], a["page"], a["max_pages"], a["Tmax"], a["d"], a["bits"], a["variant"], a["prk"], a["prv"],
@@ -82,7 +82,7 @@ def test_prefix_refusals(kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(page=8), UNSUP), (dict(page=48), UNSUP), (dict(page=512), UNSUP), (dict(n_pages=0), BAD),
-    (dict(max_pages=0), BAD), (dict(max_pages=15), BAD), (dict(table=None), BAD), (dict(table=P + 2), UNSUP)])
+    (dict(max_pages=0), BAD), (dict(max_pages=2047), BAD), (dict(table=None), BAD), (dict(table=P + 2), UNSUP)])
 def test_paged_refusals(kw, status):
     assert _paged(**kw) == status
 
@@ -130,10 +130,12 @@ def test_workspace_sizes():
     w = isoq.isoq_decode_window_workspace_size
     assert w(0, 8, 2, 256, 128, 64, 4) == 0 and w(2, 9, 2, 256, 128, 64, 4) == 0 and w(2, 8, 2, 256, 96, 64, 4) == 0
     assert w(2, 8, 2, 256, 128, -1, 0) == 0
-    small, large = w(1, 8, 2, 1 << 20, 128, 256, 4), w(1, 8, 2, 1 << 20, 128, 1 << 20, 0)
+    small, large = w(1, 8, 2, 1 << 20, 128, 8192, 4), w(1, 8, 2, 1 << 20, 128, 1 << 20, 0)
     assert 0 < small < large and small % 256 == 0
     # the work of a window does not follow the room of the cache
-    assert small == w(1, 8, 2, 1 << 24, 128, 256, 4)
+    assert small == w(1, 8, 2, 1 << 24, 128, 8192, 4)
+    # a list of seen tokens that one cluster holds needs none
+    assert w(1, 8, 2, 1 << 24, 128, 256, 4) == 0 and w(300, 8, 2, 1 << 24, 128, 256, 4) > 0
     x = isoq.isoq_decode_prefix_workspace_size
     assert x(2, 8, 2, 0, 256, 128) > 0 and x(2, 8, 2, -1, 256, 128) == 0 and x(2, 8, 2, 64, 0, 128) == 0
 
