@@ -678,16 +678,19 @@ def isoq_decode_attention_prefix(q, prefix_k, prefix_v, prefix_norms_k, prefix_n
     batch, Hkv, Tmax, pb = packed_k.shape
     heads, Tp, _ = prefix_k.shape
     index = q.get_device()
-    apart = prefix_norms_k.stride(0) if Hkv > 1 else Tp
-
-    def laid_out(x, width):   # tokens contiguous, KV heads `apart` tokens apart
-        return Tp == 0 or ((Hkv == 1 or x.stride(0) == apart * width) and (Tp == 1 or x.stride(1) == width) and
-                           (x.dim() == 2 or x.stride(2) == 1))
-
-    prefix_fits = (prefix_k.dtype is prefix_v.dtype is t.uint8 and prefix_norms_k.dtype is prefix_norms_v.dtype is t.float16 and
-                   prefix_k.shape == prefix_v.shape and prefix_norms_k.shape == prefix_norms_v.shape == prefix_k.shape[:-1]
-                   and heads == Hkv and prefix_k.shape[-1] == pb and apart >= Tp and laid_out(prefix_k, pb) and
-                   laid_out(prefix_v, pb) and laid_out(prefix_norms_k, 1) and laid_out(prefix_norms_v, 1))
+    prefix_fits = (prefix_k.dtype is prefix_v.dtype is t.uint8 and
+                   prefix_norms_k.dtype is prefix_norms_v.dtype is t.float16 and prefix_k.shape == prefix_v.shape and
+                   prefix_norms_k.shape == prefix_norms_v.shape == prefix_k.shape[:-1] and heads == Hkv and
+                   prefix_k.shape[-1] == pb)
+    apart = Tp
+    if not (prefix_k.is_contiguous() and prefix_v.is_contiguous() and prefix_norms_k.is_contiguous() and
+            prefix_norms_v.is_contiguous()):
+        # tokens contiguous, KV heads `apart` tokens apart in all four
+        apart = prefix_norms_k.stride(0) if Hkv > 1 else Tp
+        prefix_fits = prefix_fits and apart >= Tp and all(
+            Tp == 0 or ((Hkv == 1 or x.stride(0) == apart * width) and (Tp == 1 or x.stride(1) == width) and
+                        (x.dim() == 2 or x.stride(2) == 1))
+            for x, width in ((prefix_k, pb), (prefix_v, pb), (prefix_norms_k, 1), (prefix_norms_v, 1)))
     if not (batch == B and prefix_fits and prefix_len.dtype is t.int32 and prefix_len.numel() == 1 and
             _fits(q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, Hkv, d, bits, B) and
             packed_k.get_device() == packed_v.get_device() == norms_k.get_device() == norms_v.get_device() ==
@@ -736,14 +739,20 @@ def isoq_build_block_tables(seq_lens, new_lens, free_pages, block_table, page_to
         slots = n_slots
     else:
         slots = slot_map.numel()
-    ints = (seq_lens, new_lens, free_pages, block_table)
+    i32 = t.int32
     given = [x for x in (free_head, row_start, total_lens, pages_used) if x is not None]
-    if not (all(x.dtype is t.int32 and x.is_contiguous() and x.get_device() == index for x in (*ints, *given)) and
-            index >= 0 and seq_lens.numel() == B and new_lens.numel() == B and
-            (free_head is None or free_head.numel() == 1) and (row_start is None or row_start.numel() == B + 1) and
-            (total_lens is None or total_lens.numel() == B) and (pages_used is None or pages_used.numel() == 1) and
+    if not (seq_lens.dtype is i32 and new_lens.dtype is i32 and free_pages.dtype is i32 and block_table.dtype is i32 and
+            seq_lens.is_contiguous() and new_lens.is_contiguous() and free_pages.is_contiguous() and
+            block_table.is_contiguous() and
+            seq_lens.get_device() == new_lens.get_device() == free_pages.get_device() == index >= 0 and
+            seq_lens.numel() == B and new_lens.numel() == B and
+            (not given or
+             (all(x.dtype is i32 and x.is_contiguous() and x.get_device() == index for x in given) and
+              (free_head is None or free_head.numel() == 1) and (row_start is None or row_start.numel() == B + 1) and
+              (total_lens is None or total_lens.numel() == B) and (pages_used is None or pages_used.numel() == 1))) and
             (slot_map is None or (slot_map.dtype is t.int64 and slot_map.is_contiguous() and
                                   slot_map.get_device() == index and n_slots in (None, slots)))):
+        ints = (seq_lens, new_lens, free_pages, block_table)
         names = ("seq_lens", "new_lens", "free_pages", "block_table", "free_head", "row_start", "total_lens", "pages_used")
         every = (*ints, free_head, row_start, total_lens, pages_used)
         _refuse([*((n, x, t.int32) for n, x in zip(names, every)), ("slot_map", slot_map, t.int64)],

@@ -1290,7 +1290,7 @@ int launch_split_i8(const SplitArgs &a, cudaStream_t stream) {
   dim3 grid(MODE == kSplitPrefix && a.n_splits_p > a.n_splits ? a.n_splits_p : a.n_splits, a.hkv, z);
   static_assert(C::QPREP_WORDS == decode_qprep_words(D), "prepared-query layout");
   if (MODE != kSplitDense && a.fused) {
-    cudaError_t e = launch_cluster(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a, tb.lut, out_scale);
+    cudaError_t e = launch_cluster(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a.n_splits, a, tb.lut, out_scale);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "decode i8 cluster launch: %s", cudaGetErrorString(e));
   }

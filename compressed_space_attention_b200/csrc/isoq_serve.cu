@@ -28,18 +28,9 @@ namespace decode {
 #include "prefill.cuh"
 #include "serve_any.cuh"
 #include "paged.cuh"
-#include "rows_tc.cuh"
-#include "serve_prefix.cuh"
-
-// ---------------------------------------------------------------------------
-// Plans
-// ---------------------------------------------------------------------------
 
 inline int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 inline int64_t div_up(int64_t n, int64_t m) { return (n + m - 1) / m; }
-
-// Query heads of one CTA: a KV head's group, or even shares of at most 8.
-inline int row_share(int rows) { return static_cast<int>(div_up(rows, div_up(rows, 8))); }
 
 // Most 32-token blocks that a decode query sees of a row of up to `tmax`
 // tokens.
@@ -47,6 +38,16 @@ inline int64_t most_blocks(int64_t tmax, int64_t window, int64_t n_sink) {
   const int64_t all = div_up(tmax, 32), near = div_up(window, 32) + 1, sink = div_up(n_sink, 32);
   return near < all && sink < all && near + sink < all ? near + sink : all;
 }
+
+#include "rows_tc.cuh"
+#include "serve_prefix.cuh"
+
+// ---------------------------------------------------------------------------
+// Plans
+// ---------------------------------------------------------------------------
+
+// Query heads of one CTA: a KV head's group, or even shares of at most 8.
+inline int row_share(int rows) { return static_cast<int>(div_up(rows, div_up(rows, 8))); }
 
 // Tokens per split for `ctas` row groups of up to `tokens` listed tokens each:
 // the chunk that minimises the wave model of decode_chunk_tokens (4 CTAs
@@ -56,23 +57,33 @@ inline int64_t most_blocks(int64_t tmax, int64_t window, int64_t n_sink) {
 // 128 tokens per split, 16.4 at 512).  Without a window the rows are taken to
 // fill three quarters of the longest, ragged as they are (16 rows of 8,192 to
 // 16,384 tokens, 8 KV heads: 121 us at 1,024 tokens per split, 134 at the 2,048
-// that full rows would suggest).
-inline int64_t serve_chunk(int64_t ctas, int64_t tokens, bool ragged) {
-  static constexpr int64_t kChunks[] = {4096, 2560, 2048, 1536, 1280, 1024, 896, 768, 640, 512, 384, 256, 128};
-  constexpr int64_t kSms = 148, kSlots = 4, kCtaCost = 160;
-  int64_t best_chunk = kChunks[0], best_cost = -1;
-  for (const int64_t c : kChunks) {
-    int64_t n = ctas * div_up(tokens, c);
-    if (ragged && tokens > c) n = (3 * n + 3) / 4;
-    const int64_t m = div_up(n, kSms), full = m / kSlots, rest = m % kSlots;
-    const int64_t phases10 = full * (10 * kSlots + 7) + (rest ? 10 * rest + 7 : 0);
-    const int64_t cost = phases10 * ((c < tokens ? c : tokens) + kCtaCost);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best_chunk = c;
-    }
+// that full rows would suggest).  `slots`: CTAs resident per SM, 4 of the
+// integer split, 3, 2 or 1 of the CUDA-core one at d = 128, 256, 512.
+template <int64_t C>
+inline void weigh_chunk(int64_t ctas, int64_t tokens, bool ragged, int64_t slots, int64_t &best_cost, int64_t &best_chunk) {
+  constexpr int64_t kSms = 148, kCtaCost = 160;
+  int64_t n = ctas * ((tokens + C - 1) / C);
+  if (ragged && tokens > C) n = (3 * n + 3) / 4;
+  const int64_t m = (n + kSms - 1) / kSms, full = slots == 4 ? m / 4 : slots == 3 ? m / 3 : slots == 2 ? m / 2 : m;
+  const int64_t rest = m - full * slots, phases10 = full * (10 * slots + 7) + (rest ? 10 * rest + 7 : 0);
+  const int64_t cost = phases10 * ((C < tokens ? C : tokens) + kCtaCost);
+  if (best_cost < 0 || cost < best_cost) {
+    best_cost = cost;
+    best_chunk = C;
   }
-  return best_chunk;
+}
+
+// Every candidate with its divisors known to the compiler: the plan is formed
+// in each call.
+template <int64_t... C>
+inline int64_t best_chunk_of(int64_t ctas, int64_t tokens, bool ragged, int64_t slots) {
+  int64_t cost = -1, chunk = 0;
+  (weigh_chunk<C>(ctas, tokens, ragged, slots, cost, chunk), ...);
+  return chunk;
+}
+
+inline int64_t serve_chunk(int64_t ctas, int64_t tokens, bool ragged, int64_t slots) {
+  return best_chunk_of<4096, 2560, 2048, 1536, 1280, 1024, 896, 768, 640, 512, 384, 256, 128>(ctas, tokens, ragged, slots);
 }
 
 struct DecodePlan {
@@ -101,14 +112,12 @@ constexpr int kPrefixTcRows = 33;
 // prefix_max < 0: no prefix.  The list of a row is cut into the same splits
 // whatever its length.
 DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int64_t window, int64_t n_sink,
-                       bool prefix_tc = false) {
+                       bool i8, bool prefix_tc = false) {
   DecodePlan p{};
-  const int G = Hq / Hkv;
+  const int G = Hq / Hkv, slots = i8 ? 4 : (d == 128 ? 3 : (d == 256 ? 2 : 1));
   p.share = row_share(G);
   p.groups = static_cast<int>(div_up(G, p.share));
   const int64_t tokens = 32 * most_blocks(tmax, window, n_sink);
-  p.chunk = serve_chunk(static_cast<int64_t>(B) * Hkv * p.groups, tokens, window >= tmax);
-  p.splits = static_cast<int>(div_up(tokens, p.chunk));
   if (prefix_max < 0) {
     const int64_t ctas = static_cast<int64_t>(B) * Hkv * p.groups, blocks = tokens / 32, room = 4 * 148 / ctas;
     int64_t s = div_up(blocks, 4);
@@ -121,13 +130,15 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
       return p;
     }
   }
+  p.chunk = serve_chunk(static_cast<int64_t>(B) * Hkv * p.groups, tokens, window >= tmax, slots);
+  p.splits = static_cast<int>(div_up(tokens, p.chunk));
   int64_t prep_rows = static_cast<int64_t>(B) * p.groups;
   if (prefix_max >= 0) {
     const int64_t rows = static_cast<int64_t>(B) * G;
     p.share_p = row_share(static_cast<int>(rows < 8 ? rows : 8));
     p.groups_p = static_cast<int>(div_up(rows, p.share_p));
     const int64_t tp = 32 * div_up(prefix_max, 32);
-    p.chunk_p = serve_chunk(static_cast<int64_t>(Hkv) * p.groups_p, tp > 0 ? tp : 32, false);
+    p.chunk_p = serve_chunk(static_cast<int64_t>(Hkv) * p.groups_p, tp > 0 ? tp : 32, false, slots);
     p.splits_p = static_cast<int>(div_up(tp, p.chunk_p));
     prep_rows += p.groups_p;
     if (prefix_tc) {
@@ -144,11 +155,21 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
     }
   }
   p.acc_bytes = round256(static_cast<int64_t>(B) * Hq * (p.splits + p.splits_p) * (d + 2) * 4);
-  const int64_t i8 = prep_rows * Hkv * decode_qprep_words(d) * 4, any = static_cast<int64_t>(B) * Hq * d * 4;
-  p.prep_bytes = round256(i8 > any ? i8 : any);
+  p.prep_bytes = round256(i8 ? prep_rows * Hkv * decode_qprep_words(d) * 4 : static_cast<int64_t>(B) * Hq * d * 4);
   p.tiles_at = p.acc_bytes + p.prep_bytes;
   if (d != 128) p.prep_bytes += static_cast<int64_t>(p.row_tiles) * Hkv * (2 * kTcRows * 2) * d;
   return p;
+}
+
+// The most that any of these shapes' plans needs (which one runs also depends
+// on types and alignment).
+size_t most_workspace(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int64_t window, int64_t n_sink) {
+  int64_t need = 0;
+  for (int k = 0; k < (prefix_max >= 0 ? 4 : 2); ++k) {
+    const DecodePlan p = plan_decode(B, Hq, Hkv, tmax, prefix_max, d, window, n_sink, k & 1, k & 2);
+    need = p.acc_bytes + p.prep_bytes > need ? p.acc_bytes + p.prep_bytes : need;
+  }
+  return static_cast<size_t>(need);
 }
 
 // ---------------------------------------------------------------------------
@@ -165,18 +186,17 @@ int check_decode(int dtype, int B, int Hq, int Hkv, int64_t tmax, int d, int bit
     return set_error(ISOQ_ERR_INVALID_ARG, "B, Hq, Hkv and the longest row must be positive");
   if (Hq % Hkv) return set_error(ISOQ_ERR_INVALID_ARG, "Hq %% Hkv != 0");
   if (Hq / Hkv > kMaxGroup) return set_error(ISOQ_ERR_UNSUPPORTED, "Hq/Hkv > %d", kMaxGroup);
-  if (tmax >= (1ll << 31) || B > 16384 || Hkv > 65535 || Hq > (1 << 24))
+  if (tmax >= (1ll << 31) || B > 16000 || Hkv > 65535 || Hq > (1 << 24))
     return set_error(ISOQ_ERR_INVALID_ARG, "shape too large");
   if (window < 0 || n_sink < 0) return set_error(ISOQ_ERR_INVALID_ARG, "window and n_sink must not be negative");
   if (!std::isfinite(scale)) return set_error(ISOQ_ERR_INVALID_ARG, "scale is not finite");
   return ISOQ_OK;
 }
 
-int check_workspace(const void *ws, size_t bytes, const DecodePlan &p) {
-  if (p.acc_bytes + p.prep_bytes == 0) return ISOQ_OK;
+int check_workspace(const void *ws, size_t bytes, size_t need) {
+  if (need == 0) return ISOQ_OK;
   if (!ws) return set_error(ISOQ_ERR_INVALID_ARG, "workspace is NULL");
   if (!aligned(ws, 256)) return set_error(ISOQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  const size_t need = static_cast<size_t>(p.acc_bytes + p.prep_bytes);
   if (bytes < need) return set_error(ISOQ_ERR_INVALID_ARG, "workspace too small: %zu < %zu", bytes, need);
   return ISOQ_OK;
 }
@@ -205,6 +225,8 @@ int run_i8_rows(const SplitArgs &a, cudaStream_t st) {
   if (rows <= 4) return run_i8_mode<D, FULL, 4>(a, st);
   return run_i8_mode<D, FULL, 8>(a, st);
 }
+
+bool i8_split(int dtype, int d, int bits) { return dtype == ISOQ_F16 && bits == 3 && (d == 128 || d == 256); }
 
 // The bulk copies of the integer split start on 16-byte boundaries: rows of
 // a multiple of 8 tokens, norms aligned to 16 bytes.
@@ -246,7 +268,7 @@ int run_decode(SplitArgs &a, const DecodePlan &p, int dtype, int d, int bits, in
   // runs beside the split over the rows' own caches.
   if (p.row_tiles > 0 && d != 128) e = run_prep_prefix(d, variant, a, static_cast<unsigned char *>(workspace) + p.tiles_at, p.row_tiles, st);
   if (e) return e;
-  if (i8 && dtype == ISOQ_F16 && bits == 3 && (d == 128 || d == 256)) {
+  if (i8) {
     if (d == 128)
       e = variant == ISOQ_FULL ? run_i8_rows<128, true>(a, st) : run_i8_rows<128, false>(a, st);
     else
@@ -288,23 +310,14 @@ size_t isoq_decode_window_workspace_size(int B, int Hq, int Hkv, int64_t Tmax, i
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Tmax <= 0 || Tmax >= (1ll << 31) || !supported_d(d) || Hq % Hkv || window < 0 ||
       n_sink < 0)
     return 0;
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, -1, d, window, n_sink);
-  return static_cast<size_t>(p.acc_bytes + p.prep_bytes);
+  return decode::most_workspace(B, Hq, Hkv, Tmax, -1, d, window, n_sink);
 }
 
 size_t isoq_decode_prefix_workspace_size(int B, int Hq, int Hkv, int64_t prefix_tokens, int64_t Tmax, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Tmax <= 0 || Tmax >= (1ll << 31) || prefix_tokens < 0 ||
       prefix_tokens >= (1ll << 31) || !supported_d(d) || Hq % Hkv)
     return 0;
-  // The larger of the two plans (which one runs also depends on types and
-  // alignment).
-  size_t need = 0;
-  for (const bool tc : {false, true}) {
-    const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0, tc);
-    const size_t n = static_cast<size_t>(p.acc_bytes + p.prep_bytes);
-    need = n > need ? n : need;
-  }
-  return need;
+  return decode::most_workspace(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0);
 }
 
 int isoq_decode_attention_window(const void *q_dev, int dtype, const uint8_t *packed_k_dev,
@@ -323,8 +336,9 @@ int isoq_decode_attention_window(const void *q_dev, int dtype, const uint8_t *pa
       !decode::aligned(params_k_dev, 16) || !decode::aligned(params_v_dev, 16) || !decode::aligned(out_dev, 16) ||
       !decode::aligned(norms_k_dev, 2) || !decode::aligned(norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4))
     return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, -1, d, window, n_sink);
-  st = decode::check_workspace(workspace_dev, workspace_bytes, p);
+  const bool i8 = decode::i8_split(dtype, d, bits) && decode::i8_cache(norms_k_dev, norms_v_dev, Tmax);
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, -1, d, window, n_sink, i8);
+  st = decode::check_workspace(workspace_dev, workspace_bytes, decode::most_workspace(B, Hq, Hkv, Tmax, -1, d, window, n_sink));
   if (st) return st;
   decode::SplitArgs a{};
   a.mode = decode::kSplitWindow;
@@ -342,8 +356,8 @@ int isoq_decode_attention_window(const void *q_dev, int dtype, const uint8_t *pa
   a.scale = scale;
   a.window = decode::clamp31(window);
   a.n_sink = decode::clamp31(n_sink);
-  return decode::run_decode(a, p, dtype, d, bits, variant, decode::i8_cache(norms_k_dev, norms_v_dev, Tmax),
-                            params_v_dev, out_dev, workspace_dev, reinterpret_cast<cudaStream_t>(stream));
+  return decode::run_decode(a, p, dtype, d, bits, variant, i8, params_v_dev,
+                            out_dev, workspace_dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *prefix_k_dev,
@@ -377,14 +391,12 @@ int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *pr
                   prefix_tokens > 0;
   // The integer split rounds a copy of norms up to 8 tokens: within the room
   // of the last KV head only where the prefix's tokens are a multiple of 8.
-  const bool i8 = decode::i8_cache(norms_k_dev, norms_v_dev, Tmax) &&
+  const bool i8 = decode::i8_split(dtype, d, bits) && decode::i8_cache(norms_k_dev, norms_v_dev, Tmax) &&
                   (tc || (decode::i8_cache(prefix_norms_k_dev, prefix_norms_v_dev, prefix_head_stride) &&
                           prefix_tokens % 8 == 0));
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0, tc);
-  if (workspace_bytes < isoq_decode_prefix_workspace_size(B, Hq, Hkv, prefix_tokens, Tmax, d) || !workspace_dev)
-    return set_error(ISOQ_ERR_INVALID_ARG, "workspace is NULL or too small: %zu < %zu", workspace_bytes,
-                     isoq_decode_prefix_workspace_size(B, Hq, Hkv, prefix_tokens, Tmax, d));
-  st = decode::check_workspace(workspace_dev, workspace_bytes, p);
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0, i8, tc);
+  st = decode::check_workspace(workspace_dev, workspace_bytes,
+                               decode::most_workspace(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0));
   if (st) return st;
   decode::SplitArgs a{};
   a.mode = tc ? decode::kSplitWindow : decode::kSplitPrefix;
@@ -437,8 +449,10 @@ int isoq_paged_decode_attention(const void *q_dev, int dtype, const uint8_t *pag
       !decode::aligned(norms_k_dev, 2) || !decode::aligned(norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4) ||
       !decode::aligned(block_table_dev, 4))
     return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, max_len, -1, d, window, n_sink);
-  st = decode::check_workspace(workspace_dev, workspace_bytes, p);
+  const bool i8 = decode::i8_split(dtype, d, bits) && decode::i8_cache(norms_k_dev, norms_v_dev, 8);
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, max_len, -1, d, window, n_sink, i8);
+  st = decode::check_workspace(workspace_dev, workspace_bytes,
+                               decode::most_workspace(B, Hq, Hkv, max_len, -1, d, window, n_sink));
   if (st) return st;
   decode::SplitArgs a{};
   a.mode = decode::kSplitPaged;
@@ -460,8 +474,8 @@ int isoq_paged_decode_attention(const void *q_dev, int dtype, const uint8_t *pag
   a.page_shift = shift;
   a.max_pages = max_pages;
   a.n_pages = n_pages;
-  return decode::run_decode(a, p, dtype, d, bits, variant, decode::i8_cache(norms_k_dev, norms_v_dev, 8),
-                            params_v_dev, out_dev, workspace_dev, reinterpret_cast<cudaStream_t>(stream));
+  return decode::run_decode(a, p, dtype, d, bits, variant, i8, params_v_dev,
+                            out_dev, workspace_dev, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int isoq_prefill_attention_window(const void *q_dev, int dtype, const uint8_t *packed_k_dev,

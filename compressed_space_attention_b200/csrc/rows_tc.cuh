@@ -36,8 +36,12 @@
 // times the operator's arithmetic).
 //
 // kPfWindow: rows are positions x heads of a chunk; rotation of the queries
-// before and of the output after the loop, both in the CTA.  kPfPrefix: rows
-// are a KV head's batch x group; one partial state per row and split.
+// before and of the output after the loop, both in the CTA.  Where the chunk
+// has fewer row tiles than there are SMs, a cluster of CTAs shares the tokens
+// of a row tile and merges its partial states in shared memory (256 queries,
+// 32 over 4 heads, window 1,024: 39.4 us with one CTA per row tile, @CL@ with
+// two).  kPfPrefix: rows are a KV head's batch x group; one partial state per
+// row and split.
 //
 // Every wait is bounded.  A role whose wait gives up records kErrWaitTimeout
 // and stops; the others' waits then run out as well, the products already
@@ -102,7 +106,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int qt = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int ranks = WIN ? static_cast<int>(cluster_size()) : 1, rank = WIN ? static_cast<int>(cluster_rank()) : 0;
+  const int qt = WIN ? blockIdx.x / ranks : blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int G = a.group;
 
   // ---- the CTA's rows and tokens ----
@@ -113,7 +118,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   const int tq0 = WIN ? qt * per_cta : 0;
   const int p_first = WIN ? *lens - a.tq + tq0 : 0;          // position of the CTA's first row
   const int total_rows = WIN ? 0 : a.batch * G;
-  int tend, t_base = 0, n_sink_tiles = 0, win_tile = 0, n_iter;
+  int tend, t_base = 0, n_sink_tiles = 0, win_tile = 0, n_iter, j_base = 0;
   if constexpr (WIN) {
     int p_last = p_first + per_cta - 1;
     if (tq0 + per_cta > a.tq) p_last = *lens - 1;
@@ -129,13 +134,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
       win_tile = lo / kRowsTok > n_sink_tiles ? lo / kRowsTok : n_sink_tiles;
       n_iter = n_sink_tiles + (all > win_tile ? all - win_tile : 0);
     }
+    // This CTA's share of the cluster's tiles.
+    j_base = n_iter * rank / ranks;
+    n_iter = n_iter * (rank + 1) / ranks - j_base;
   } else {
     const long long first = static_cast<long long>(b) * a.chunk;
     t_base = first < len ? static_cast<int>(first) : len;
     tend = len - t_base > a.chunk ? t_base + a.chunk : len;
     n_iter = (tend - t_base + kRowsTok - 1) / kRowsTok;
   }
-  auto tile_t0 = [&](int j) { return WIN ? kRowsTok * (j < n_sink_tiles ? j : j - n_sink_tiles + win_tile) : t_base + kRowsTok * j; };
+  auto tile_t0 = [&](int j) {
+    if constexpr (WIN) {
+      const int v = j_base + j;
+      return kRowsTok * (v < n_sink_tiles ? v : v - n_sink_tiles + win_tile);
+    } else {
+      return t_base + kRowsTok * j;
+    }
+  };
   // Row i of the CTA: its query (row of q and out), or -1.
   auto query_of = [&](int i) -> long long {
     if constexpr (WIN) {
@@ -387,10 +402,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
     named_barrier(1 + (warp & 3), 64);
     l += xchg[(half ^ 1) * kTcRows + i];
     if constexpr (WIN) {
-      // O / l into shared memory over the K and V buffers: row i, 16-byte chunk
-      // c at c ^ (i mod 32) (no bank conflicts for a thread per row here, a
-      // warp per row below)
-      const float inv = l > 0.f ? a.out_unit / (l * v_scale) : 0.f;
+      // O into shared memory over the K and V buffers: row i, 16-byte chunk c at
+      // c ^ (i mod 32) (no bank conflicts for a thread per row here, a warp per
+      // row below); (r, l) beside it, over the norms
+      const float inv = 1.f / v_scale;
+      if (half == 0) reinterpret_cast<float2 *>(norms)[i] = make_float2(ref, l);
       float4 *dst = reinterpret_cast<float4 *>(smem) + 32 * i;
 #pragma unroll 1
       for (int c = 4 * half; c < 4 * half + 4; ++c) {
@@ -579,13 +595,38 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   __syncthreads();
 
   if constexpr (WIN) {
-    // ---- inverse rotation, one warp per row (lane: 4 dims) ----
+    // ---- merge over the cluster in rank order and rotate back: one warp per
+    // row (lane: 4 dims), the rows dealt out over the CTAs ----
+    if (ranks > 1) cluster_sync();
     const float *prm = a.params_v + static_cast<size_t>(kvh) * 256 + 8 * lane;
     const Quat ql = load_quat(prm), qr = load_quat(prm + 4);
-    for (int i = warp; i < kTcRows; i += kRowsWarps) {
+    for (int i = rank + ranks * warp; i < kTcRows; i += ranks * kRowsWarps) {
       const long long row = query_of(i);
       if (row < 0) continue;   // warp-uniform
-      const float4 u = reinterpret_cast<const float4 *>(smem)[32 * i + (lane ^ (i & 31))];
+      float l = 0.f;
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ranks == 1) {
+        l = norms[2 * i + 1];
+        u = reinterpret_cast<const float4 *>(smem)[32 * i + (lane ^ (i & 31))];
+      } else {
+      const float2 mine = lane < ranks ? peer_load2(peer_address(norms + 2 * i, lane)) : make_float2(-INFINITY, 0.f);
+      float m = mine.x;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = __shfl_sync(0xffffffffu, m, 0);
+      const float w_mine = mine.x == -INFINITY ? 0.f : ex2f(mine.x - m);
+      for (int k = 0; k < ranks; ++k) {
+        const float4 v = peer_load4(peer_address(smem + 16 * (32 * i + (lane ^ (i & 31))), k));
+        const float w = __shfl_sync(0xffffffffu, w_mine, k);
+        l = fmaf(__shfl_sync(0xffffffffu, mine.y, k), w, l);
+        u.x = fmaf(v.x, w, u.x);
+        u.y = fmaf(v.y, w, u.y);
+        u.z = fmaf(v.z, w, u.z);
+        u.w = fmaf(v.w, w, u.w);
+      }
+      }
+      const float inv = l > 0.f ? a.out_unit / l : 0.f;
+      u = make_float4(u.x * inv, u.y * inv, u.z * inv, u.w * inv);
       const Quat r = block_inverse(ql, qr, Quat{u.x, u.y, u.z, u.w}, FULL);
       const float y0 = r.w + r.x, y1 = r.w - r.x, y2 = r.y + r.z, y3 = r.y - r.z;
       float x[4] = {y0 + y2, y1 + y3, y0 - y2, y1 - y3};
@@ -598,6 +639,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
       *reinterpret_cast<uint2 *>(static_cast<__half *>(a.out) + row * 128 + 4 * lane) =
           make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]));
     }
+    if (ranks > 1) cluster_sync();   // no CTA ends while its shared memory is read
   } else {
     // This grid overlaps the split over the rows' own caches, launched before
     // it; the combine waits for this grid, so this grid ends after that one.
@@ -610,16 +652,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   }
 }
 
+// `ranks` (kPfWindow): CTAs of the cluster that shares a row tile's tokens.
 template <int KIND, bool FULL>
-int launch_rows_tc(const PrefillArgs &a, dim3 grid, cudaStream_t st) {
+int launch_rows_tc(const PrefillArgs &a, dim3 grid, int ranks, cudaStream_t st) {
   auto kernel = rows_tc_kernel<KIND, FULL>;
   const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg::SMEM);
   if (c != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "attention (128 rows): %s", cudaGetErrorString(c));
   cudaError_t e = cudaSuccess;
   if (KIND == kPfPrefix)
     e = launch_pdl(kernel, grid, dim3(kRowsThreads), RowsCfg::SMEM, st, a);
-  else
+  else if (ranks == 1)
     kernel<<<grid, kRowsThreads, RowsCfg::SMEM, st>>>(a);
+  else
+    e = launch_cluster(kernel, dim3(grid.x * ranks, grid.y, grid.z), dim3(kRowsThreads), RowsCfg::SMEM, st, ranks, a);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "attention (128 rows) launch: %s", cudaGetErrorString(e));
 }

@@ -487,7 +487,7 @@ int launch_split_any(const SplitArgs &a, cudaStream_t st) {
   const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (c != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "split: %s", cudaGetErrorString(c));
   if (a.fused) {
-    cudaError_t e = launch_cluster(kernel, dim3(a.n_splits, a.hkv, group_count(a, a.mode)), dim3(kAnyThreads), C::SMEM, st, a);
+    cudaError_t e = launch_cluster(kernel, dim3(a.n_splits, a.hkv, group_count(a, a.mode)), dim3(kAnyThreads), C::SMEM, st, a.n_splits, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "split cluster launch: %s", cudaGetErrorString(e));
   }

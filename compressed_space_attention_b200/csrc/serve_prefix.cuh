@@ -115,7 +115,7 @@ int run_prefix_tc(int d, int variant, const SplitArgs &a, const unsigned char *t
   prefill_tables(p, d);
   if (d == 256) return launch_prefix_tc<256>(p, splits, st);
   const dim3 grid(static_cast<unsigned>(row_tiles), static_cast<unsigned>(a.hkv), static_cast<unsigned>(splits));
-  return variant == ISOQ_FULL ? launch_rows_tc<kPfPrefix, true>(p, grid, st) : launch_rows_tc<kPfPrefix, false>(p, grid, st);
+  return variant == ISOQ_FULL ? launch_rows_tc<kPfPrefix, true>(p, grid, 1, st) : launch_rows_tc<kPfPrefix, false>(p, grid, 1, st);
 }
 
 // Windowed chunked prefill at d = 128.
@@ -123,5 +123,12 @@ int run_window_rows(int variant, PrefillArgs a, cudaStream_t st) {
   prefill_tables(a, 128);
   const int per = kTcRows / a.group;
   const dim3 grid(static_cast<unsigned>((a.tq + per - 1) / per), static_cast<unsigned>(a.hkv), static_cast<unsigned>(a.batch));
-  return variant == ISOQ_FULL ? launch_rows_tc<kPfWindow, true>(a, grid, st) : launch_rows_tc<kPfWindow, false>(a, grid, st);
+  // CTAs per row tile: as many as the SMs hold at once, at most 8, each with
+  // two tiles of tokens or more (of the most that a row tile can see).
+  const int64_t ctas = static_cast<int64_t>(grid.x) * grid.y * grid.z;
+  const int64_t tiles = most_blocks(a.tmax, static_cast<int64_t>(a.window) + per, a.n_sink) / 4 + 1;
+  int64_t ranks = 148 / ctas < kMaxClusterSplits ? 148 / ctas : kMaxClusterSplits;
+  ranks = ranks < tiles / 2 ? ranks : tiles / 2;
+  const int n = ranks > 1 ? static_cast<int>(ranks) : 1;
+  return variant == ISOQ_FULL ? launch_rows_tc<kPfWindow, true>(a, grid, n, st) : launch_rows_tc<kPfWindow, false>(a, grid, n, st);
 }

@@ -350,7 +350,7 @@ int isoq_prefill_attention(const void *q_dev, int dtype, const uint8_t *packed_k
  *   window, n_sink  >= 0; values above Tmax count as Tmax (no window).
  *   workspace_dev   at least isoq_decode_window_workspace_size(...) bytes
  *                   (a function of the same arguments), 256-byte aligned.
- * The other arguments and rules as isoq_decode_attention; B <= 16384.
+ * The other arguments and rules as isoq_decode_attention; B <= 16000.
  * Float16 queries with 3-bit codes, d in {128, 256}, Tmax % 8 == 0 and norms
  * aligned to 16 bytes take the integer tensor-core split, everything else a
  * float32 one.  isoq_decode_window_workspace_size returns 0 on invalid shapes,
@@ -394,7 +394,7 @@ int isoq_prefill_attention_window(const void *q_dev, int dtype, const uint8_t *p
  *   prefix_len_dev  one int32 on the device.
  *   workspace_dev   at least isoq_decode_prefix_workspace_size(...) bytes.
  * prefix_tokens = 0 is allowed (the prefix pointers may then be NULL).  The
- * other arguments and rules as isoq_decode_attention; B <= 16384.  The
+ * other arguments and rules as isoq_decode_attention; B <= 16000.  The
  * tensor-core splits need what isoq_decode_attention_window names, for
  * prefix_head_stride and prefix_tokens too.
  */
