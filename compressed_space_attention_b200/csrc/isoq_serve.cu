@@ -102,12 +102,20 @@ struct DecodePlan {
 // Small problems run as one launch: up to 8 splits of a row group form a
 // cluster that merges its partial states itself.  Taken where 8 splits of at
 // most 16 blocks cover the longest list and all CTAs are resident at once (4 per
-// SM): 1 row, 32 query over 4 KV heads, 1,028 tokens: @FUSED@ us against 10.3 us for the three launches.
+// SM).  1 row, 32 query over 4 KV heads, 1,028 tokens: 12.3 us on the GPU
+// against 10.3 for the three launches, but 5.3 us of host time to queue it
+// against 9.9 (and no workspace): with the Python call around it a step of many
+// layers is bound by the queueing, 13.4 us a call against 19.2.
 constexpr int kFusedSplits = kMaxClusterSplits, kFusedBlocks = 16;
 
-// Which prefix split: rows of a KV head's batch x group from which on the
-// tcgen05 one is faster (float16 queries, 3-bit codes, d = 128 or 256).
-constexpr int kPrefixTcRows = 33;
+// The rows of a KV head's batch x group from which on the prefix goes to the
+// tcgen05 split (float16 queries, 3-bit codes).  Its time hardly depends on the
+// rows of a 128-row tile, the integer split's goes with every 8.  Integer and
+// tcgen05 split, 4 KV heads, us: d = 128, 8,192 tokens: 8 rows 20.5, 20.5, 16
+// rows 22.6, 20.6; 65,536 tokens: 8 rows 39.0, 47.2, 16 rows 63.6, 55.4, 64
+// rows 167, 58.6.  d = 256, 8,192 tokens: 16 rows 36.4, 39.0, 32 rows 43.9,
+// 41.0; 65,536 tokens: 16 rows 113, 139, 32 rows 201, 142.
+constexpr int prefix_tc_rows(int d) { return d == 128 ? 9 : 24; }
 
 // prefix_max < 0: no prefix.  The list of a row is cut into the same splits
 // whatever its length.
@@ -387,7 +395,7 @@ int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *pr
       !decode::aligned(prefix_norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4) || !decode::aligned(prefix_len_dev, 4))
     return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
   // The tcgen05 split reads codes and norms by plain loads: any prefix does.
-  const bool tc = decode::tc_prefix(dtype, d, bits) && B * static_cast<int64_t>(Hq / Hkv) >= decode::kPrefixTcRows &&
+  const bool tc = decode::tc_prefix(dtype, d, bits) && B * static_cast<int64_t>(Hq / Hkv) >= decode::prefix_tc_rows(d) &&
                   prefix_tokens > 0;
   // The integer split rounds a copy of norms up to 8 tokens: within the room
   // of the last KV head only where the prefix's tokens are a multiple of 8.

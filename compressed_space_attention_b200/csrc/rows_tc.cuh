@@ -39,7 +39,7 @@
 // before and of the output after the loop, both in the CTA.  Where the chunk
 // has fewer row tiles than there are SMs, a cluster of CTAs shares the tokens
 // of a row tile and merges its partial states in shared memory (256 queries,
-// 32 over 4 heads, window 1,024: 39.4 us with one CTA per row tile, @CL@ with
+// 32 over 4 heads, window 1,024: 39.4 us with one CTA per row tile, 30.8 with
 // two).  kPfPrefix: rows are a KV head's batch x group; one partial state per
 // row and split.
 //
@@ -84,10 +84,16 @@ __device__ __forceinline__ void tc_ld32_done(uint32_t (&r)[32]) {
                       "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+__device__ __forceinline__ void tc_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Bits 0 .. n - 1.
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
 
-template <int KIND, bool FULL>
+template <int KIND, bool FULL, bool CLUSTER = false>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillArgs a) {
   using C = RowsCfg;
   constexpr bool WIN = KIND == kPfWindow;
@@ -106,8 +112,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ranks = WIN ? static_cast<int>(cluster_size()) : 1, rank = WIN ? static_cast<int>(cluster_rank()) : 0;
-  const int qt = WIN ? blockIdx.x / ranks : blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int ranks = CLUSTER ? static_cast<int>(cluster_size()) : 1, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+  const int qt = CLUSTER ? blockIdx.x / ranks : blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int G = a.group;
 
   // ---- the CTA's rows and tokens ----
@@ -135,8 +141,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
       n_iter = n_sink_tiles + (all > win_tile ? all - win_tile : 0);
     }
     // This CTA's share of the cluster's tiles.
-    j_base = n_iter * rank / ranks;
-    n_iter = n_iter * (rank + 1) / ranks - j_base;
+    if constexpr (CLUSTER) {
+      j_base = n_iter * rank / ranks;
+      n_iter = n_iter * (rank + 1) / ranks - j_base;
+    }
   } else {
     const long long first = static_cast<long long>(b) * a.chunk;
     t_base = first < len ? static_cast<int>(first) : len;
@@ -357,23 +365,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
       const float base = ref == -INFINITY ? 0.f : ref;
       const uint64_t base2 = f2_pack(base, base);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const ulonglong2 *v4 = reinterpret_cast<const ulonglong2 *>(nv + 32 * c);
-        uint32_t hi[16], lo[16];
+      for (int c = 0; c < 4; ++c) {   // 16 scores: 8 columns of hi and 8 of lo parts
+        const ulonglong2 *v4 = reinterpret_cast<const ulonglong2 *>(nv + 16 * c);
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 4; ++k) {
           const ulonglong2 w = v4[k];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int q = 4 * k + 2 * e;
+            const int q = 16 * (c & 1) + 4 * k + 2 * e;
             float x0, x1, w0, w1, d0, d1;
-            f2_unpack(f2_sub(f2_pack(x[c][q], x[c][q + 1]), base2), x0, x1);
+            f2_unpack(f2_sub(f2_pack(x[c >> 1][q], x[c >> 1][q + 1]), base2), x0, x1);
             const uint64_t p2 = f2_pack(ex2f(x0), ex2f(x1));
             if (e) lb = f2_add(lb, p2); else la = f2_add(la, p2);
             f2_unpack(f2_mul(p2, e ? w.y : w.x), w0, w1);
             if (part) {   // a token that is not seen weighs nothing, whatever its norm holds
-              w0 = (vis[c] >> q) & 1u ? w0 : 0.f;
-              w1 = (vis[c] >> (q + 1)) & 1u ? w1 : 0.f;
+              w0 = (vis[c >> 1] >> q) & 1u ? w0 : 0.f;
+              w1 = (vis[c >> 1] >> (q + 1)) & 1u ? w1 : 0.f;
             }
             const __half2 h = __floats2half2_rn(w0, w1);
             const float2 hf = __half22float2(h);
@@ -382,8 +390,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
             lo[2 * k + e] = pack_f16x2(d0, d1);
           }
         }
-        tc_st16u(t_s + 32 * c, hi);
-        tc_st16u(t_s + 32 * c + 16, lo);
+        tc_st8u(t_s + 32 * (c >> 1) + 8 * (c & 1), hi);
+        tc_st8u(t_s + 32 * (c >> 1) + 16 + 8 * (c & 1), lo);
       }
       tc_wait_st();
       tc_fence_before();
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   if constexpr (WIN) {
     // ---- merge over the cluster in rank order and rotate back: one warp per
     // row (lane: 4 dims), the rows dealt out over the CTAs ----
-    if (ranks > 1) cluster_sync();
+    if constexpr (CLUSTER) cluster_sync();
     const float *prm = a.params_v + static_cast<size_t>(kvh) * 256 + 8 * lane;
     const Quat ql = load_quat(prm), qr = load_quat(prm + 4);
     for (int i = rank + ranks * warp; i < kTcRows; i += ranks * kRowsWarps) {
@@ -605,7 +613,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
       if (row < 0) continue;   // warp-uniform
       float l = 0.f;
       float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (ranks == 1) {
+      if constexpr (!CLUSTER) {
         l = norms[2 * i + 1];
         u = reinterpret_cast<const float4 *>(smem)[32 * i + (lane ^ (i & 31))];
       } else {
@@ -639,7 +647,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
       *reinterpret_cast<uint2 *>(static_cast<__half *>(a.out) + row * 128 + 4 * lane) =
           make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]));
     }
-    if (ranks > 1) cluster_sync();   // no CTA ends while its shared memory is read
+    if constexpr (CLUSTER) cluster_sync();   // no CTA ends while its shared memory is read
   } else {
     // This grid overlaps the split over the rows' own caches, launched before
     // it; the combine waits for this grid, so this grid ends after that one.
@@ -656,6 +664,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
 template <int KIND, bool FULL>
 int launch_rows_tc(const PrefillArgs &a, dim3 grid, int ranks, cudaStream_t st) {
   auto kernel = rows_tc_kernel<KIND, FULL>;
+  if constexpr (KIND == kPfWindow)
+    if (ranks > 1) kernel = rows_tc_kernel<KIND, FULL, true>;
   const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg::SMEM);
   if (c != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "attention (128 rows): %s", cudaGetErrorString(c));
   cudaError_t e = cudaSuccess;
