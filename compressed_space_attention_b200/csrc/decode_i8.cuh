@@ -1270,18 +1270,9 @@ int launch_split_i8(const SplitArgs &a, cudaStream_t stream) {
   // in the modes other than kSplitDense.)
   constexpr bool SF = MODE == kSplitDense ? FULL : true;
   auto kernel = slices ? split_i8_kernel<D, SF, GP, true, MODE> : split_i8_kernel<D, SF, GP, false, MODE>;
-  static bool configured = false;
-  static std::mutex mu;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!configured) {
-      for (auto k : {split_i8_kernel<D, SF, GP, true, MODE>, split_i8_kernel<D, SF, GP, false, MODE>}) {
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-        if (e != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "decode i8: %s", cudaGetErrorString(e));
-      }
-      configured = true;
-    }
-  }
+  static std::atomic<unsigned long long> allowed[2];
+  cudaError_t e = allow_smem(allowed[slices], reinterpret_cast<const void *>(kernel), C::SMEM);
+  if (e != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "decode i8: %s", cudaGetErrorString(e));
   const I8Tables &tb = i8_tables();
   const double unit = 1.0 / (tb.scale * std::sqrt(static_cast<double>(D)));
   const float score_unit = static_cast<float>(a.scale * unit * 1.4426950408889634);
@@ -1290,12 +1281,12 @@ int launch_split_i8(const SplitArgs &a, cudaStream_t stream) {
   dim3 grid(MODE == kSplitPrefix && a.n_splits_p > a.n_splits ? a.n_splits_p : a.n_splits, a.hkv, z);
   static_assert(C::QPREP_WORDS == decode_qprep_words(D), "prepared-query layout");
   if (MODE != kSplitDense && a.fused) {
-    cudaError_t e = launch_cluster(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a.n_splits, a, tb.lut, out_scale);
+    e = launch_cluster(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a.n_splits, a, tb.lut, out_scale);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "decode i8 cluster launch: %s", cudaGetErrorString(e));
   }
   prep_i8_kernel<D, FULL, GP, MODE><<<dim3(a.hkv, z), 32 * GP, 0, stream>>>(a, score_unit);
-  cudaError_t e = launch_pdl(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a, tb.lut, out_scale);
+  e = launch_pdl(kernel, grid, dim3(kI8Threads), C::SMEM, stream, a, tb.lut, out_scale);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "decode i8 launch: %s", cudaGetErrorString(e));
   return ISOQ_OK;

@@ -702,20 +702,13 @@ template <typename T, int D, bool FULL, int GP, int KIND>
 int launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream) {
   using C = TcCfg<D>;
   auto kernel = prefill_tc_kernel<T, D, FULL, GP, KIND>;
-  static bool configured = false;
-  static std::mutex mu;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!configured) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-      if (e != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "prefill (tcgen05): %s", cudaGetErrorString(e));
-      configured = true;
-    }
-  }
+  static std::atomic<unsigned long long> allowed;
+  cudaError_t e = allow_smem(allowed, reinterpret_cast<const void *>(kernel), C::SMEM);
+  if (e != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "prefill (tcgen05): %s", cudaGetErrorString(e));
   constexpr int BQ = kTcRows / GP;
   dim3 grid((a.tq + BQ - 1) / BQ, a.hkv, a.batch);
   kernel<<<grid, kTcThreads, C::SMEM, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "prefill (tcgen05) launch: %s", cudaGetErrorString(e));
   return ISOQ_OK;
 }

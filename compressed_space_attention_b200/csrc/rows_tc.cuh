@@ -666,7 +666,8 @@ int launch_rows_tc(const PrefillArgs &a, dim3 grid, int ranks, cudaStream_t st) 
   auto kernel = rows_tc_kernel<KIND, FULL>;
   if constexpr (KIND == kPfWindow)
     if (ranks > 1) kernel = rows_tc_kernel<KIND, FULL, true>;
-  const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg::SMEM);
+  static std::atomic<unsigned long long> allowed[2];
+  const cudaError_t c = allow_smem(allowed[ranks > 1], reinterpret_cast<const void *>(kernel), RowsCfg::SMEM);
   if (c != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "attention (128 rows): %s", cudaGetErrorString(c));
   cudaError_t e = cudaSuccess;
   if (KIND == kPfPrefix)

@@ -484,7 +484,8 @@ template <int D, int BITS, int RG>
 int launch_split_any(const SplitArgs &a, cudaStream_t st) {
   using C = AnyCfg<D, BITS, RG>;
   auto kernel = split_any_kernel<D, BITS, RG>;
-  const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<unsigned long long> allowed;
+  const cudaError_t c = allow_smem(allowed, reinterpret_cast<const void *>(kernel), C::SMEM);
   if (c != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "split: %s", cudaGetErrorString(c));
   if (a.fused) {
     cudaError_t e = launch_cluster(kernel, dim3(a.n_splits, a.hkv, group_count(a, a.mode)), dim3(kAnyThreads), C::SMEM, st, a.n_splits, a);

@@ -82,7 +82,8 @@ template <int D>
 int launch_prefix_tc(const PrefillArgs &p, int splits, cudaStream_t st) {
   using C = TcCfg<D>;
   auto kernel = prefill_tc_kernel<__half, D, true, 1, kPfPrefix>;
-  const cudaError_t c = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<unsigned long long> allowed;
+  const cudaError_t c = allow_smem(allowed, reinterpret_cast<const void *>(kernel), C::SMEM);
   if (c != cudaSuccess) return set_error(ISOQ_ERR_CUDA, "prefix: %s", cudaGetErrorString(c));
   cudaError_t e = launch_pdl(kernel, dim3(p.row_tiles, p.hkv, splits), dim3(kTcThreads), C::SMEM, st, p);
   if (e == cudaSuccess) e = cudaGetLastError();

@@ -541,3 +541,120 @@ def test_outputs_and_workspaces_end_where_they_say():
     assert (ws[n:] == 77).all() and (out[b] == 5).all() and (out[:b] != 5).all()
     with pytest.raises(isoq.IsoqError, match="workspace too small"):
         isoq.isoq_decode_attention_window(q, *cache, lens, *par, 4, 0, 8000, 7, workspace=ws[:n - 256])
+
+
+@pytest.mark.parametrize("dtype,d,bits,hq,hkv", [(F16, 128, 3, 8, 2), (F16, 256, 3, 4, 2), (F32, 128, 4, 6, 2)])
+@pytest.mark.parametrize("p", [16, 64])
+def test_what_lies_behind_a_row_is_ignored(dtype, d, bits, hq, hkv, p):
+    """NaN and infinite norms behind each row's end, in its last page and in the
+    pages of no row, and behind the prefix's length."""
+    g = np.random.default_rng(p + d)
+    lens = np.array([1, 37, 130, 0], np.int32)
+    b, tmax, room = len(lens), 160, 96
+    pages, table = _pages(g, lens, hkv, d, bits, p, -(-tmax // p))
+    cache, prefix = _cache(g, (b, hkv, tmax), d, bits), _cache(g, (hkv, room), d, bits)
+    par = _params(hkv, d, 0)
+    q = g.standard_normal((b, hq, d)).astype(dtype)
+    scale = 1 / np.sqrt(d)
+    bad_pages, bad_cache, bad_prefix = ([x.copy() for x in c] for c in (pages, cache, prefix))
+    used = np.zeros(pages[0].shape[0] * p, bool)
+    for i, t in enumerate(lens):
+        for j in range(t):
+            used[table[i, j // p] * p + j % p] = True
+        bad_cache[2][i][:, t:], bad_cache[3][i][:, t:] = np.nan, np.inf
+    off = ~used.reshape(-1, p)
+    for h in range(hkv):
+        bad_pages[2][:, h][off], bad_pages[3][:, h][off] = np.inf, np.nan
+    bad_prefix[2][:, 61:], bad_prefix[3][:, 61:] = np.nan, np.inf
+    dl, dp = _t(lens), [_t(x) for x in par]
+    got = isoq.isoq_paged_decode_attention(_t(q), *map(_t, bad_pages), _t(table), dl, *dp, bits, 0)
+    _check(got, S.paged_decode(q, pages, table, lens, *par, bits, 0, scale, tmax, 1 << 30, 0), dtype, q, pages[2], pages[3], scale)
+    got = isoq.isoq_decode_attention_prefix(_t(q), *map(_t, bad_prefix), _t(np.array([61], np.int32)), *map(_t, bad_cache), dl,
+                                            *dp, bits, 0)
+    _check(got, S.prefix_decode(q, prefix, 61, *cache, lens, *par, bits, 0, scale), dtype, q,
+           np.concatenate([prefix[2].ravel(), cache[2].ravel()]), np.concatenate([prefix[3].ravel(), cache[3].ravel()]), scale)
+
+
+def test_two_calls_at_once_and_the_same_bits_every_time():
+    """Calls on two streams at once, each with its own output: the bits of the
+    same calls one after the other, and of a second round."""
+    g = np.random.default_rng(12)
+    d, hq, hkv, b, tmax = 128, 32, 4, 6, 6144
+    lens = np.full(b, 6000, np.int32)
+    cache, prefix = [_t(c) for c in _cache(g, (b, hkv, tmax), d, 3)], [_t(c) for c in _cache(g, (hkv, 4096), d, 3)]
+    par, dl = [_t(x) for x in _params(hkv, d, 0)], _t(lens)
+    plen = torch.tensor([4000], dtype=torch.int32, device=DEV)
+    q = _t(g.standard_normal((b, hq, d)).astype(F16))
+    qc = _t(g.standard_normal((b, 40, hq, d)).astype(F16))
+    calls = [lambda: isoq.isoq_decode_attention_window(q, *cache, dl, *par, 3, 0, 5000, 64),
+             lambda: isoq.isoq_decode_attention_window(q, *cache, dl, *par, 3, 0, 700, 3),
+             lambda: isoq.isoq_decode_attention_prefix(q, *prefix, plen, *cache, dl, *par, 3, 0),
+             lambda: isoq.isoq_prefill_attention_window(qc, *cache, dl, *par, 3, 0, 600, 5)]
+    alone = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        outs = []
+        for s, f in zip(streams, calls):
+            with torch.cuda.stream(s):
+                outs.append(f())
+        torch.cuda.synchronize()
+        for a, o in zip(alone, outs):
+            assert torch.equal(a, o)
+    assert isoq.isoq_check_device_error() == 0
+
+
+def test_offsets_beyond_32_bits():
+    """Pages and rows more than 4 GiB into their pool: the bits of the same
+    tokens in a small one."""
+    g = np.random.default_rng(13)
+    d, bits, hq, hkv, p, b = 256, 3, 16, 8, 256, 2
+    lens = np.array([700, 300], np.int32)
+    small = [_t(x) for x in _cache(g, (6, hkv, p), d, bits)]
+    table = _t(np.array([[0, 1, 2], [3, 4, 5]], np.int32))
+    n = 24000                                    # 4.7 GB of packed K
+    large = [torch.empty((n, *x.shape[1:]), dtype=x.dtype, device=DEV) for x in small]
+    for x, y in zip(large, small):
+        x[-6:] = y
+    par, dl = [_t(x) for x in _params(hkv, d, 0)], _t(lens)
+    for dtype in (F16, F32):
+        q = _t(g.standard_normal((b, hq, d)).astype(dtype))
+        a = isoq.isoq_paged_decode_attention(q, *small, table, dl, *par, bits, 0)
+        c = isoq.isoq_paged_decode_attention(q, *large, table + (n - 6), dl, *par, bits, 0)
+        assert torch.equal(a, c)
+    kv = _t(g.standard_normal((2, 3, hkv, d)).astype(F16))
+    slot = torch.tensor([5, 700, 1100], dtype=torch.int64, device=DEV)
+    isoq.isoq_paged_append(kv[0], kv[1], *small, slot, *par, bits, 0)
+    isoq.isoq_paged_append(kv[0], kv[1], *large, slot + (n - 6) * p, *par, bits, 0)
+    for x, y in zip(large, small):
+        assert torch.equal(x[-6:].contiguous().view(torch.uint8), y.view(torch.uint8))
+    del large
+    # one row of 6.3 million tokens x 8 heads, of which the last are seen
+    t, near = 6291456, 640
+    row = [torch.empty((1, hkv, t, *x.shape[3:]), dtype=x.dtype, device=DEV) for x in small]
+    tail = [x.reshape(6, hkv, p, *x.shape[3:])[:3].transpose(0, 1).reshape(1, hkv, 3 * p, *x.shape[3:]).contiguous() for x in small]
+    for x, y in zip(row, tail):
+        x[:, :, -3 * p:] = y
+    q = _t(g.standard_normal((1, hq, d)).astype(F16))
+    one = torch.ones(1, dtype=torch.int32, device=DEV)
+    a = isoq.isoq_decode_attention_window(q, *tail, one * (3 * p), *par, bits, 0, near)
+    c = isoq.isoq_decode_attention_window(q, *row, one * t, *par, bits, 0, near)
+    assert torch.equal(a, c)
+    qc = _t(g.standard_normal((1, 20, hq, d)).astype(F16))
+    a = isoq.isoq_prefill_attention_window(qc, *tail, one * (3 * p), *par, bits, 0, near)
+    c = isoq.isoq_prefill_attention_window(qc, *row, one * t, *par, bits, 0, near)
+    assert (a.float() - c.float()).abs().max() <= 2e-3
+    assert isoq.isoq_check_device_error() == 0
+
+
+def test_append_of_a_slot_map_longer_than_the_tokens():
+    g = np.random.default_rng(14)
+    pages = _cache(g, (2, 1, 16), 128, 3)
+    dev, par = [_t(x) for x in pages], _params(1, 128, 0)
+    kv = g.standard_normal((2, 3, 1, 128)).astype(F16)
+    slot = np.array([4, -1, 31, 9, 9], np.int64)
+    isoq.isoq_paged_append(_t(kv[0]), _t(kv[1]), *dev, _t(slot), *map(_t, par), 3, 0)
+    isoq.isoq_paged_append(_t(kv[0][:0]), _t(kv[1][:0]), *dev, _t(slot), *map(_t, par), 3, 0)
+    assert isoq.isoq_check_device_error() == 0
+    for got, want in zip(dev, S.paged_append(kv[0], kv[1], pages, slot[:3], *par, 3, 0)):
+        np.testing.assert_array_equal(got.cpu().numpy().view(np.uint8), want.view(np.uint8))
