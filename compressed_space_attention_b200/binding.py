@@ -767,17 +767,14 @@ def isoq_build_block_tables(seq_lens, new_lens, free_pages, block_table, page_to
     if t.cuda.current_device() != index:
         return _elsewhere(isoq_build_block_tables, index, seq_lens, new_lens, free_pages, block_table, page_tokens, n_slots,
                           free_head, slot_map, row_start, total_lens, pages_used, stream)
-    dev = block_table.device
     if slot_map is None:
-        slot_map = t.empty(slots, dtype=t.int64, device=dev)
-    if row_start is None and total_lens is None and pages_used is None:   # one allocation
-        row_start, total_lens, pages_used = t.empty(2 * B + 2, dtype=t.int32, device=dev).split((B + 1, B, 1))
+        slot_map = block_table.new_empty(slots, dtype=t.int64)
     if row_start is None:
-        row_start = t.empty(B + 1, dtype=t.int32, device=dev)
+        row_start = block_table.new_empty(B + 1)
     if total_lens is None:
-        total_lens = t.empty(B, dtype=t.int32, device=dev)
+        total_lens = block_table.new_empty(B)
     if pages_used is None:
-        pages_used = t.empty(1, dtype=t.int32, device=dev)
+        pages_used = block_table.new_empty(1)
     st = lib().isoq_build_block_tables(
         seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), _ptr(free_head), free_pages.numel(), B,
         page_tokens, max_pages, block_table.data_ptr(), slots, slot_map.data_ptr(), row_start.data_ptr(),

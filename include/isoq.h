@@ -384,8 +384,9 @@ int isoq_prefill_attention_window(const void *q_dev, int dtype, const uint8_t *p
  * Decode of a batch whose rows share a prefix.  Row b attends to the first
  * P = min(max(*prefix_len_dev, 0), prefix_tokens) tokens of one packed prefix
  * and to its own T_b = min(max(seq_lens[b], 0), Tmax) tokens, under one
- * softmax; the prefix is unpacked once for all rows of the batch (up to 8
- * query heads at a time), not once per row.  Both parts use the same rotation
+ * softmax.  The prefix is unpacked once for 128 query rows of a KV head (batch
+ * rows x heads; float16 queries, 3 bits, from 9 rows on at d = 128 and 24 at
+ * d = 256) or once for 8, not once per row.  Both parts use the same rotation
  * parameters.
  *   prefix_k_dev, prefix_v_dev  [Hkv] rows of prefix_head_stride packed
  *                vectors, of which the first prefix_tokens may be read;
