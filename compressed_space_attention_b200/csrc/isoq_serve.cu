@@ -59,7 +59,7 @@ inline int row_share(int rows) { return static_cast<int>(div_up(rows, div_up(row
 // fill three quarters of the longest, ragged as they are (16 rows of 8,192 to
 // 16,384 tokens, 8 KV heads: 121 us at 1,024 tokens per split, 134 at the 2,048
 // that full rows would suggest).  `slots`: CTAs resident per SM, 4 of the
-// integer split, 3, 2 or 1 of the CUDA-core one at d = 128, 256, 512.
+// integer split, 4, 2 or 1 of the CUDA-core one at d = 128, 256, 512.
 template <int64_t C>
 inline void weigh_chunk(int64_t ctas, int64_t tokens, bool ragged, int64_t slots, int64_t &best_cost, int64_t &best_chunk) {
   constexpr int64_t kSms = 148, kCtaCost = 160;
@@ -123,7 +123,7 @@ constexpr int prefix_tc_rows(int d) { return d == 128 ? 9 : 24; }
 DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int64_t window, int64_t n_sink,
                        bool i8, bool prefix_tc = false) {
   DecodePlan p{};
-  const int G = Hq / Hkv, slots = i8 ? 4 : (d == 128 ? 3 : (d == 256 ? 2 : 1));
+  const int G = Hq / Hkv, slots = i8 || d == 128 ? 4 : (d == 256 ? 2 : 1);
   p.share = row_share(G);
   p.groups = static_cast<int>(div_up(G, p.share));
   const int64_t tokens = 32 * most_blocks(tmax, window, n_sink);

@@ -17,12 +17,14 @@
 //   (RG rows of one dimension, broadcast over t) serves four tokens, every
 //   centroid it looks up RG rows, two per f32x2 instruction.  Two exchanges
 //   add the four slices and leave lane L with token L.
-//   Values: a lane takes 8 or 16 dimensions (at d = 128 half a warp per token,
-//   two tokens at a time), the weights broadcast.
+//   Values: a lane takes d / 32 dimensions, the weights broadcast.
 //
-// Bound: shared-memory loads (a lookup per code and lane, weights and queries)
-// and the FMA pipe, about 10 and 8 cycles of an SM per token, KV head and 8
-// rows at d = 128.
+// Bound: issue slots and the ALU pipe (0.57 per cycle and 46 % busy): about 110
+// warp instructions per token and KV head for 8 rows, of which the two products
+// are 32, the code lookups 32.  16 rows of 4,096 to 8,192 tokens x 4 KV heads,
+// d = 128, 4 bits, 8 rows: a token per lane in the score loop took 92 us (every
+// query value loaded again for each token), this form 78; half a warp per token
+// in the value loop 84 (168 registers, 3 CTAs per SM instead of 4).
 
 constexpr int kAnyWarps = 4;
 constexpr int kAnyThreads = 32 * kAnyWarps;
@@ -39,7 +41,7 @@ struct AnyCfg {
   static constexpr int OFF_W = OFF_Q + (D / 32) * Q_GROUP * 4;      // [warp][32][RG] weights
   static constexpr int OFF_TAB = OFF_W + kAnyWarps * 32 * RG * 4;   // [16] centroids
   static constexpr int OFF_ML = OFF_TAB + 16 * 4;           // [warp][RG] (m, l)
-  static constexpr int PVL = D == 128 ? 16 : 32;            // lanes per token in the value loop
+  static constexpr int MIN_BLOCKS = D == 128 ? 4 : 1;       // by shared memory: 4, 2 and 1 at d = 128, 256, 512
   static constexpr int SMEM = OFF_ML + kAnyWarps * RG * 8;
   static_assert(kAnyWarps * RG * D * 4 <= OFF_Q, "the warps' accumulators fit the stages");
 };
@@ -131,9 +133,9 @@ __global__ void __launch_bounds__(128) prep_rotate_kernel(const SplitArgs a) {
 }
 
 template <int D, int BITS, int RG>
-__global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs a) {
+__global__ void __launch_bounds__(kAnyThreads, AnyCfg<D, BITS, RG>::MIN_BLOCKS) split_any_kernel(const SplitArgs a) {
   using C = AnyCfg<D, BITS, RG>;
-  constexpr int PB = C::PB, RS = C::RS, PVL = C::PVL, KD = D / PVL, RP = RG / 2;
+  constexpr int PB = C::PB, RS = C::RS, KD = D / 32, RP = RG / 2;
   extern __shared__ __align__(128) unsigned char smem[];
   float *qs = reinterpret_cast<float *>(smem + C::OFF_Q);
   unsigned char *tab = smem + C::OFF_TAB;
@@ -366,12 +368,9 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
 
     // ---- values: this lane's dimensions over the block's tokens; a token that
     // is not seen has weight 0 (and codes of whatever the stage held) ----
-    constexpr int TPW = 32 / PVL;                    // tokens at a time
-    const int th = lane / PVL, vl = lane % PVL;
     const int n_tok = 32 - __clz(mask);              // past the last token seen
 #pragma unroll 2
-    for (int j0 = 0; j0 < n_tok; j0 += TPW) {
-      const int j = j0 + th;
+    for (int j = 0; j < n_tok; ++j) {
       uint64_t w2[RP];
       if constexpr (RG >= 4) {
 #pragma unroll
@@ -386,7 +385,7 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
       const uint32_t *vr = reinterpret_cast<const uint32_t *>(vc + j * RS);
 #pragma unroll
       for (int u = 0; u < KD / 4; ++u) {
-        const uint32_t f = quad_fields<BITS>(vr, (KD / 4) * vl + u);
+        const uint32_t f = quad_fields<BITS>(vr, (KD / 4) * lane + u);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float c = *reinterpret_cast<const float *>(tab + (e == 0 ? (f << 2) & 0x3Cu : (f >> (4 * e - 2)) & 0x3Cu));
@@ -407,12 +406,6 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
     for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
     if (lane == 0) ml[warp * RG + r] = make_float2(m[r], l[r]);
   }
-  if constexpr (PVL == 16) {   // the two half warps' tokens
-#pragma unroll
-    for (int k = 0; k < KD; ++k)
-#pragma unroll
-      for (int r = 0; r < RP; ++r) acc[k][r] = f2_add(acc[k][r], __shfl_xor_sync(0xffffffffu, acc[k][r], 16));
-  }
   __syncthreads();   // every warp is done with its stages
   float *sl = reinterpret_cast<float *>(smem);   // [warp][RG][D]
 #pragma unroll
@@ -421,10 +414,8 @@ __global__ void __launch_bounds__(kAnyThreads) split_any_kernel(const SplitArgs 
     for (int k = 0; k < KD; ++k) {
       float u0, u1;
       f2_unpack(acc[k][r], u0, u1);
-      if (PVL == 32 || lane < 16) {
-        sl[(warp * RG + 2 * r) * D + KD * (lane % PVL) + k] = u0;
-        sl[(warp * RG + 2 * r + 1) * D + KD * (lane % PVL) + k] = u1;
-      }
+      sl[(warp * RG + 2 * r) * D + KD * lane + k] = u0;
+      sl[(warp * RG + 2 * r + 1) * D + KD * lane + k] = u1;
     }
   }
   __syncthreads();
