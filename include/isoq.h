@@ -429,10 +429,11 @@ int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *pr
  *   slot_map_dev     [n_slots] int64: the slots of all new tokens, row after
  *                    row, then -1.
  *   row_start_dev    [B + 1] int32: where a row's new tokens begin in
- *                    slot_map; the last entry is their number.
+ *                    slot_map; the last entry is their number (at most
+ *                    2^31 - 1).
  *   total_lens_dev   [B] int32: seq_lens + new_lens.
  *   pages_used_dev   one int32: pages taken (what a caller adds to its head).
- * A row that does not fit (more tokens than the table row or slot_map holds,
+ * A row that does not fit (more tokens than the table row, an int32 or slot_map holds,
  * new_lens[b] < 0, or a free list that the pages up to its own exhaust) takes
  * no page: its slots are -1, total_lens[b] is seq_lens[b], and the next
  * isoq_check_device_error reports ISOQ_ERR_INVALID_ARG.  No output may overlap

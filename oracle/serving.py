@@ -97,7 +97,7 @@ def block_tables(seq_lens, new_lens, free_pages, page_tokens, block_table, n_slo
         n = max(new, 0)
         first = row_start[-1]
         row_start.append(first + n)
-        fits = new >= 0 and length + new <= table.shape[1] * p and (n == 0 or first + n <= n_slots)
+        fits = new >= 0 and length + new <= min(table.shape[1] * p, 2 ** 31 - 1) and (n == 0 or first + n <= n_slots)
         have, need = -(-length // p), -(-(length + n) // p)
         take = need - have if fits else 0
         if fits and (take == 0 or free_head + taken + take <= len(free_pages)):
@@ -112,7 +112,7 @@ def block_tables(seq_lens, new_lens, free_pages, page_tokens, block_table, n_slo
             failed.append(b)
             total.append(length)
         taken += take
-    return table, slot_map, np.array(row_start, np.int32), np.array(total, np.int32), used, failed
+    return table, slot_map, np.array([min(x, 2 ** 31 - 1) for x in row_start], np.int32), np.array(total, np.int32), used, failed
 
 
 def paged_append(k_new, v_new, pages, slot_map, params_k, params_v, bits, variant):

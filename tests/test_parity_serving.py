@@ -110,7 +110,7 @@ def test_window_decode_odd_rooms_and_norm_offsets(tmax, dtype):
         flat = torch.empty(dev[i].numel() + 1, dtype=torch.float16, device=DEV)
         flat[1:] = dev[i].reshape(-1)
         dev[i] = flat[1:].view(b, hkv, tmax)
-    for window, n_sink in [(0, 0), (0, 3), (5, 0), (tmax, 1)]:
+    for window, n_sink in [(0, 0), (0, 3), (5, 0), (tmax, 1), (2 ** 63 - 1, 2 ** 63 - 1)]:
         got = isoq.isoq_decode_attention_window(_t(q), *dev, _t(lens), *map(_t, par), bits, 0, window, n_sink, scale=0.05)
         ref = S.window_decode(q, *cache, lens, *par, bits, 0, 0.05, window, n_sink)
         _check(got, ref, dtype, q, cache[2], cache[3], 0.05)
@@ -658,3 +658,21 @@ def test_append_of_a_slot_map_longer_than_the_tokens():
     assert isoq.isoq_check_device_error() == 0
     for got, want in zip(dev, S.paged_append(kv[0], kv[1], pages, slot[:3], *par, 3, 0)):
         np.testing.assert_array_equal(got.cpu().numpy().view(np.uint8), want.view(np.uint8))
+
+
+def test_block_tables_of_lengths_near_the_largest():
+    """Lengths and sums of new tokens next to and beyond 2^31: those requests
+    do not fit, and nothing overflows."""
+    free = np.arange(8, dtype=np.int32)
+    lens = np.array([2 ** 31 - 1, 2 ** 31 - 200, 10, 0], np.int32)
+    new = np.array([1, 150, 2 ** 31 - 1, 3], np.int32)
+    table = np.full((4, 2), 5, np.int32)
+    dt = _t(table)
+    out = isoq.isoq_build_block_tables(_t(lens), _t(new), _t(free), dt, 256, 2000)
+    ref = S.block_tables(lens, new, free, 256, table, 2000)
+    assert isoq.isoq_check_device_error() == isoq.ISOQ_ERR_INVALID_ARG
+    np.testing.assert_array_equal(dt.cpu().numpy(), ref[0])
+    np.testing.assert_array_equal(out[0].cpu().numpy(), ref[1])
+    np.testing.assert_array_equal(out[1].cpu().numpy(), ref[2])
+    np.testing.assert_array_equal(out[2].cpu().numpy(), ref[3])
+    assert int(out[3]) == ref[4]

@@ -134,6 +134,8 @@ def test_workspace_sizes():
     assert 0 < small < large and small % 256 == 0
     # the work of a window does not follow the room of the cache
     assert small == w(1, 8, 2, 1 << 24, 128, 8192, 4)
+    # windows and sinks beyond the room are the room, up to the largest integer
+    assert w(3, 8, 2, 9000, 128, 2 ** 63 - 1, 2 ** 63 - 1) == w(3, 8, 2, 9000, 128, 9000, 0)
     # a list of seen tokens that one cluster holds needs none
     assert w(1, 8, 2, 1 << 24, 128, 256, 4) == 0 and w(300, 8, 2, 1 << 24, 128, 256, 4) > 0
     x = isoq.isoq_decode_prefix_workspace_size
