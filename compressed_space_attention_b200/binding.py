@@ -2,9 +2,13 @@
 
 Every function here has the name of the C entry point it calls.  Tensors
 provide device memory and strides; the current torch CUDA stream of the
-tensors' device is passed as the stream.  All computation happens in the
-library's CUDA kernels: there is no CPU or Python fallback, and a missing
-library raises at import of this module's functions.
+tensors' device is passed as the stream, or the one that ``stream`` names (a
+torch stream or its handle).  What a call allocates belongs to the stream that
+it launches on, as under ``torch.cuda.stream``; ordering that stream with the
+ones that write the inputs and read the outputs is the caller's, as there.
+All computation happens in the library's CUDA kernels: there is no CPU or
+Python fallback, and a missing library raises at import of this module's
+functions.
 """
 
 from __future__ import annotations
@@ -222,6 +226,20 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _empty(shape, dtype, dev, stream=None):
+    """torch.empty from the pool of the stream that the call launches on.  From
+    another stream's pool the memory could be handed out again as soon as the
+    call has returned, or still be in use there, while the kernels work on it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(dev, stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def isoq_quantize(x, params, bits: int, variant: int, codes=None, norms=None,
                   out_head_stride: Optional[int] = None, stream=None):
     """Compresses x [n_heads][n_vec][d] (or [n_vec][d]); returns (codes, norms).
@@ -239,9 +257,9 @@ def isoq_quantize(x, params, bits: int, variant: int, codes=None, norms=None,
     dev = _require_cuda(x, params, codes, norms)
     pb = isoq_packed_bytes(d, bits)
     if codes is None:
-        codes = torch.empty((n_heads, n_vec, pb), dtype=torch.uint8, device=dev)
+        codes = _empty((n_heads, n_vec, pb), torch.uint8, dev, stream)
     if norms is None:
-        norms = torch.empty((n_heads, n_vec), dtype=torch.float16, device=dev)
+        norms = _empty((n_heads, n_vec), torch.float16, dev, stream)
     if out_head_stride is None:
         out_head_stride = n_vec
     with torch.cuda.device(dev):
@@ -262,7 +280,7 @@ def isoq_dequantize(codes, norms, params, d: int, bits: int, variant: int, out_d
     n_heads, n_vec, _ = codes.shape
     dev = _require_cuda(codes, norms, params, out)
     if out is None:
-        out = torch.empty((n_heads, n_vec, d), dtype=out_dtype or torch.float32, device=dev)
+        out = _empty((n_heads, n_vec, d), out_dtype or torch.float32, dev, stream)
     if in_head_stride is None:
         in_head_stride = n_vec
     with torch.cuda.device(dev):
@@ -288,7 +306,7 @@ def isoq_prefill_attention(q, packed_k, packed_v, norms_k, norms_v, seq_lens, pa
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, Tq, Hq, d), dtype=q.dtype, device=dev)
+        out = _empty((B, Tq, Hq, d), q.dtype, dev, stream)
     with torch.cuda.device(dev):
         st = lib().isoq_prefill_attention(
             _ptr(q), _dtype_code(q), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v),
@@ -324,9 +342,9 @@ def isoq_rotor_quantize(x, rotors, bits: int, codes=None, norms=None, stream=Non
         raise ValueError("the last dimension of x must be contiguous")
     dev = _require_cuda(x, rotors, codes, norms)
     if codes is None:
-        codes = torch.empty((n_heads, n_vec, isoq_rotor_packed_bytes(d, bits)), dtype=torch.uint8, device=dev)
+        codes = _empty((n_heads, n_vec, isoq_rotor_packed_bytes(d, bits)), torch.uint8, dev, stream)
     if norms is None:
-        norms = torch.empty((n_heads, n_vec), dtype=torch.float16, device=dev)
+        norms = _empty((n_heads, n_vec), torch.float16, dev, stream)
     with torch.cuda.device(dev):
         st = lib().isoq_rotor_quantize(_ptr(x), _dtype_code(x), n_heads, n_vec, d, bits, x.stride(0),
                                        x.stride(1), _ptr(rotors), _ptr(codes), _ptr(norms), n_vec,
@@ -344,7 +362,7 @@ def isoq_rotor_dequantize(codes, norms, rotors, d: int, bits: int, out_dtype=Non
     n_heads, n_vec, _ = codes.shape
     dev = _require_cuda(codes, norms, rotors, out)
     if out is None:
-        out = torch.empty((n_heads, n_vec, d), dtype=out_dtype or torch.float32, device=dev)
+        out = _empty((n_heads, n_vec, d), out_dtype or torch.float32, dev, stream)
     with torch.cuda.device(dev):
         st = lib().isoq_rotor_dequantize(_ptr(codes), _ptr(norms), n_heads, n_vec, d, bits, n_vec,
                                          _ptr(rotors), _ptr(out), _dtype_code(out), out.stride(0),
@@ -372,10 +390,10 @@ def isoq_decode_attention(q, packed_k, packed_v, norms_k, norms_v, seq_lens, par
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=q.dtype, device=dev)
+        out = _empty((B, Hq, d), q.dtype, dev, stream)
     ws_bytes = isoq_decode_workspace_size(B, Hq, Hkv, Tmax, d)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(ws_bytes, torch.uint8, dev, stream)
     with torch.cuda.device(dev):
         st = lib().isoq_decode_attention(
             _ptr(q), _dtype_code(q), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v),
@@ -417,10 +435,10 @@ def isoq_decode_step(q, k_new, v_new, packed_k, packed_v, norms_k, norms_v, seq_
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=q.dtype, device=dev)
+        out = _empty((B, Hq, d), q.dtype, dev, stream)
     ws_bytes = isoq_decode_workspace_size(B, Hq, Hkv, Tmax, d)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(ws_bytes, torch.uint8, dev, stream)
     with torch.cuda.device(dev):
         st = lib().isoq_decode_step(
             _ptr(q), _ptr(k_new), _ptr(v_new), _dtype_code(q), _ptr(packed_k), _ptr(packed_v),
@@ -498,7 +516,7 @@ def isoq_decode_attention_static(q, packed_k, packed_v, norms_k, norms_v, seq_le
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, Hq, d), dtype=q.dtype, device=dev)
+        out = _empty((B, Hq, d), q.dtype, dev, stream)
     with torch.cuda.device(dev):
         st = lib().isoq_decode_attention_static(
             _ptr(q), _dtype_code(q), _ptr(packed_k), _ptr(packed_v), _ptr(norms_k), _ptr(norms_v),
@@ -570,17 +588,17 @@ def _given_out(out, q):
         raise ValueError("all tensors must be on the same device")
 
 
-def _scratch(workspace, nbytes, dev):
+def _scratch(workspace, nbytes, dev, stream):
     """Address and bytes of the caller's workspace, or of one from torch's
-    allocator (returned too: it lives until the launch is queued)."""
+    allocator (returned too: it lives until the launch is queued, after which
+    its stream's order keeps it)."""
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.device != dev:
             raise ValueError("workspace must be contiguous and on the device of q")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if nbytes == 0:
         return None, None, 0
-    t = _torch()
-    workspace = t.empty(nbytes, dtype=t.uint8, device=dev)
+    workspace = _empty(nbytes, _torch().uint8, dev, stream)
     return workspace, workspace.data_ptr(), nbytes
 
 
@@ -619,10 +637,10 @@ def isoq_decode_attention_window(q, packed_k, packed_v, norms_k, norms_v, seq_le
         return _elsewhere(isoq_decode_attention_window, index, q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k,
                           params_v, bits, variant, window, n_sink, scale, out, workspace, stream)
     if out is None:
-        out = t.empty_like(q)
+        out = t.empty_like(q) if stream is None else _empty(q.shape, q.dtype, q.device, stream)
     else:
         _given_out(out, q)
-    workspace, wp, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink), q.device)
+    workspace, wp, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, Tmax, d, window, n_sink), q.device, stream)
     st = lib().isoq_decode_attention_window(
         q.data_ptr(), _dtype_code(q), packed_k.data_ptr(), packed_v.data_ptr(), norms_k.data_ptr(), norms_v.data_ptr(),
         seq_lens.data_ptr(), B, Hq, Hkv, Tmax, d, bits, variant, params_k.data_ptr(), params_v.data_ptr(),
@@ -653,7 +671,7 @@ def isoq_prefill_attention_window(q, packed_k, packed_v, norms_k, norms_v, seq_l
         return _elsewhere(isoq_prefill_attention_window, index, q, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k,
                           params_v, bits, variant, window, n_sink, scale, out, stream)
     if out is None:
-        out = t.empty_like(q)
+        out = t.empty_like(q) if stream is None else _empty(q.shape, q.dtype, q.device, stream)
     else:
         _given_out(out, q)
     st = lib().isoq_prefill_attention_window(
@@ -709,10 +727,10 @@ def isoq_decode_attention_prefix(q, prefix_k, prefix_v, prefix_norms_k, prefix_n
                           prefix_len, packed_k, packed_v, norms_k, norms_v, seq_lens, params_k, params_v, bits, variant,
                           scale, out, workspace, stream)
     if out is None:
-        out = t.empty_like(q)
+        out = t.empty_like(q) if stream is None else _empty(q.shape, q.dtype, q.device, stream)
     else:
         _given_out(out, q)
-    workspace, wp, ws = _scratch(workspace, isoq_decode_prefix_workspace_size(B, Hq, Hkv, Tp, Tmax, d), q.device)
+    workspace, wp, ws = _scratch(workspace, isoq_decode_prefix_workspace_size(B, Hq, Hkv, Tp, Tmax, d), q.device, stream)
     st = lib().isoq_decode_attention_prefix(
         q.data_ptr(), _dtype_code(q), prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_norms_k.data_ptr(),
         prefix_norms_v.data_ptr(), prefix_len.data_ptr(), Tp, apart, packed_k.data_ptr(), packed_v.data_ptr(),
@@ -768,13 +786,13 @@ def isoq_build_block_tables(seq_lens, new_lens, free_pages, block_table, page_to
         return _elsewhere(isoq_build_block_tables, index, seq_lens, new_lens, free_pages, block_table, page_tokens, n_slots,
                           free_head, slot_map, row_start, total_lens, pages_used, stream)
     if slot_map is None:
-        slot_map = block_table.new_empty(slots, dtype=t.int64)
+        slot_map = _empty(slots, t.int64, block_table.device, stream)
     if row_start is None:
-        row_start = block_table.new_empty(B + 1)
+        row_start = _empty(B + 1, i32, block_table.device, stream)
     if total_lens is None:
-        total_lens = block_table.new_empty(B)
+        total_lens = _empty(B, i32, block_table.device, stream)
     if pages_used is None:
-        pages_used = block_table.new_empty(1)
+        pages_used = _empty(1, i32, block_table.device, stream)
     st = lib().isoq_build_block_tables(
         seq_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), _ptr(free_head), free_pages.numel(), B,
         page_tokens, max_pages, block_table.data_ptr(), slots, slot_map.data_ptr(), row_start.data_ptr(),
@@ -853,10 +871,10 @@ def isoq_paged_decode_attention(q, pages_k, pages_v, norms_k, norms_v, block_tab
         return _elsewhere(isoq_paged_decode_attention, index, q, pages_k, pages_v, norms_k, norms_v, block_table, seq_lens,
                           params_k, params_v, bits, variant, max_len, window, n_sink, scale, out, workspace, stream)
     if out is None:
-        out = t.empty_like(q)
+        out = t.empty_like(q) if stream is None else _empty(q.shape, q.dtype, q.device, stream)
     else:
         _given_out(out, q)
-    workspace, wp, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, max_len, d, window, n_sink), q.device)
+    workspace, wp, ws = _scratch(workspace, isoq_decode_window_workspace_size(B, Hq, Hkv, max_len, d, window, n_sink), q.device, stream)
     st = lib().isoq_paged_decode_attention(
         q.data_ptr(), _dtype_code(q), pages_k.data_ptr(), pages_v.data_ptr(), norms_k.data_ptr(), norms_v.data_ptr(),
         block_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, n_pages, P, max_pages, max_len, d, bits, variant,
