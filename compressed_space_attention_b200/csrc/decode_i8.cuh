@@ -479,15 +479,18 @@ __global__ void __launch_bounds__(kI8Threads, I8Cfg<D, GP>::MIN_BLOCKS)
   const uint16_t *nvb = (over_prefix ? a.prefix_nv : a.norms_v) + cache0;
 
   // kSplitPaged: the pages of the split's blocks, one entry per block, two
-  // where a page holds 16 tokens; -1 past the row's end.
+  // where a page holds 16 tokens; -1 for a half whose page the query sees no
+  // token of (past the row's end, behind the window): its table entry is not
+  // followed and nothing is copied.
   __shared__ int page_of[MODE == kSplitPaged ? kPagedChunkMax / 16 : 1];
   const int unit_shift = MODE == kSplitPaged && a.page_shift == 4 ? 1 : 0;
   if constexpr (MODE == kSplitPaged) {
     bool bad = false;
     for (int u = tid; u < n_blk << unit_shift; u += kI8Threads) {
-      const int t = kBlk * block_at(v0 + (u >> unit_shift)) + 16 * (u & unit_shift);
+      const int blk = block_at(v0 + (u >> unit_shift)), t = kBlk * blk + 16 * (u & unit_shift);
+      const unsigned unit_mask = (seen_mask(seen, blk) >> (16 * (u & unit_shift))) & (unit_shift ? 0xFFFFu : 0xFFFFFFFFu);
       int page = -1;
-      if (t < tlen) {
+      if (unit_mask) {
         page = a.block_table[static_cast<long long>(row) * a.max_pages + (t >> a.page_shift)];
         if (page < 0 || page >= a.n_pages) {   // reported; page 0 stands in
           page = 0;

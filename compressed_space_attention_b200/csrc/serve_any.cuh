@@ -162,10 +162,14 @@ __global__ void __launch_bounds__(kAnyThreads, AnyCfg<D, BITS, RG>::MIN_BLOCKS) 
   const long long cache0 = paged ? 0 : grp.prefix ? kvh * a.head_stride : (static_cast<long long>(row) * a.hkv + kvh) * a.tmax;
 
   // Cache row of token t (the same for 16 tokens from a multiple of 16 on,
-  // plus t mod 16).  A page index out of range is reported; page 0 stands in.
+  // plus t mod 16).  Where the query sees none of those tokens (which a page of
+  // 16 may hold alone) the table is not followed; a page index out of range is
+  // reported.  Page 0 stands in for both.
   auto row16 = [&](int t) -> long long {
     if (!paged) return cache0 + t;
-    int page = a.block_table[static_cast<long long>(row) * a.max_pages + (t >> a.page_shift)];
+    int page = 0;
+    if (a.page_shift > 4 || t < seen.sink || max(t, seen.lo) < min(t + 16, seen.len))
+      page = a.block_table[static_cast<long long>(row) * a.max_pages + (t >> a.page_shift)];
     if (page < 0 || page >= a.n_pages) {
       atomicOr(&g_decode_error, kErrBadPage);
       page = 0;

@@ -8,7 +8,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import compressed_space_attention_b200 as isoq  # noqa: E402
-from test_parity_serving import DEV, F16, _cache, _pages, _params, _t  # noqa: E402
+from oracle import serving as S  # noqa: E402
+from test_parity_serving import DEV, F16, F32, _cache, _check, _pages, _params, _t  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,38 @@ def test_stream_argument_without_workspace(raw):
         for a, o in zip(alone, outs):
             assert torch.equal(a, o)
     assert isoq.isoq_check_device_error() == 0
+
+
+def _drop_unseen_pages(table, lens, p, max_len, window, n_sink, fill):
+    """The table with `fill` at every page that holds no token its row's query sees."""
+    out = table.copy()
+    for b, t in enumerate(lens):
+        t = min(max(int(t), 0), max_len)
+        pages = {j // p for j in S.seen_tokens(t - 1, t, window, n_sink)}
+        out[b, [c for c in range(table.shape[1]) if c not in pages]] = fill
+    return out
+
+
+@pytest.mark.parametrize("p", [16, 32])
+@pytest.mark.parametrize("dtype,d,bits,hq,hkv", [(F16, 128, 3, 8, 2), (F16, 256, 3, 2, 2), (F32, 128, 4, 6, 2),
+                                                 (F16, 512, 2, 4, 1)])
+def test_pages_that_no_query_sees_are_not_followed(dtype, d, bits, hq, hkv, p):
+    """Pages behind the window and between it and the sinks are gone from the
+    table (-1, or an index beyond the pool): no error, the same outputs, in
+    one launch and in many splits."""
+    g = np.random.default_rng(p + d)
+    tmax = 6400
+    lens = np.array([333, 48, 17, 1, 0, 640, 5000, 6399], np.int32)
+    cols = tmax // p
+    pages, table = _pages(g, lens, hkv, d, bits, p, cols)
+    par = _params(hkv, d, 0)
+    q = g.standard_normal((len(lens), hq, d)).astype(dtype)
+    dev, dpar, scale = [_t(x) for x in pages], [_t(x) for x in par], 1 / np.sqrt(d)
+    for window, n_sink, fill in [(1, 0, -1), (17, 0, 1 << 30), (40, 5, -1), (100, 16, -1), (15, 33, 1 << 30), (4200, 17, -1)]:
+        rows = np.arange(len(lens)) if window > 1000 else np.arange(6)
+        max_len = tmax if window > 1000 else 640
+        gone = _drop_unseen_pages(table, lens, p, max_len, window, n_sink, fill)
+        got = isoq.isoq_paged_decode_attention(_t(q[rows]), *dev, _t(gone[rows]), _t(lens[rows]), *dpar, bits, 0,
+                                               max_len=max_len, window=window, n_sink=n_sink)
+        ref = S.paged_decode(q[rows], pages, table[rows], lens[rows], *par, bits, 0, scale, max_len, window, n_sink)
+        _check(got, ref, dtype, q, pages[2], pages[3], scale)
