@@ -18,6 +18,7 @@
 #include <atomic>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "tcgen05.cuh"
@@ -171,7 +172,7 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
   p.acc_bytes = round256(static_cast<int64_t>(B) * Hq * (p.splits + p.splits_p) * (d + 2) * 4);
   p.prep_bytes = round256(i8 ? prep_rows * Hkv * decode_qprep_words(d) * 4 : static_cast<int64_t>(B) * Hq * d * 4);
   p.tiles_at = p.acc_bytes + p.prep_bytes;
-  if (d != 128) p.prep_bytes += static_cast<int64_t>(p.row_tiles) * Hkv * (2 * kTcRows * 2) * d;
+  if (d == 256) p.prep_bytes += static_cast<int64_t>(p.row_tiles) * Hkv * TcCfg<256>::Q_TILE;
   return p;
 }
 

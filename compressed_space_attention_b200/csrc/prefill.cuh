@@ -1,7 +1,7 @@
 // Causal attention of a chunk of Tq new queries over the packed cache
 // (chunked prefill), on the 5th-generation tensor cores (tcgen05 + TMEM).
-// Included by isoq_decode.cu inside namespace isoq::decode, after the
-// rotation helpers.
+// Included by isoq_decode.cu and isoq_serve.cu inside namespace isoq::decode,
+// after the rotation helpers.
 //
 // Query t of batch row b sits at position p = seq_lens[b] - Tq + t and
 // attends to the cached tokens j <= p (RotaryQuant §3.4: kernel A with
@@ -21,7 +21,8 @@
 //   searched on the host; the residuals are below 2^-15 of the centroids,
 //   so hi + lo keeps them to about 2^-26), and one thread issues
 //   S(j + 1) = Q~hi K~hi^T + Q~lo K~hi^T + Q~hi K~lo^T (tcgen05.mma
-//   kind::f16, M = 128, N = 64; q~ split into float16 hi and lo parts) into
+//   kind::f16, M = 128, N = 64; q~ split into float16 hi and lo parts, each
+//   row scaled by a power of two: query_scale) into
 //   the other of two TMEM S buffers, so it runs under the softmax of tile j;
 //   each thread reads its half row of S(j) (tcgen05.ld), scales it by
 //   s^K scale / alpha, masks it on diagonal tiles, exchanges its half-row
@@ -72,7 +73,8 @@ struct PrefillArgs {
   uint32_t res_lo0, res_lo1, res_hi0, res_hi1;   // float16 alpha c_k - fp16(alpha c_k), low / high bytes
   int window, n_sink;             // kPfWindow: tokens j > p - window or j < n_sink only
   // kPfPrefix: query rows prepared in the operand layout, [Hkv][row tiles] of
-  // float16 hi and lo tiles; partial states as the decode's splits write them.
+  // float16 hi and lo tiles and the rows' inverse scales (TcCfg::Q_TILE bytes);
+  // partial states as the decode's splits write them.
   const unsigned char *q_tiles;
   const int32_t *prefix_len;
   long long head_stride;          // tokens between KV heads
@@ -90,6 +92,20 @@ enum PrefillKind { kPfCausal = 0, kPfWindow = 1, kPfPrefix = 2 };
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The scale of a query row's float16 hi and lo parts, and its inverse, which
+// the row's scores take: 1 while the largest rotated component `mx` lies in
+// [1/4, 2^15), else the power of two that takes it to [2^14, 2^15).  A rotated
+// component can reach |q|, sqrt(d) times what float16 holds, and below 1/4 the
+// lo parts lose bits to the subnormal numbers (steps of 2^-24); so hi + lo
+// keeps 22 bits of every row.  (The exponent is kept from 64 on, for zeros and
+// for what cancels to next to nothing.)
+__device__ __forceinline__ float query_scale(float mx, float &inverse) {
+  uint32_t e = __float_as_uint(mx) >> 23;
+  e = e < 64u ? 64u : (e >= 125u && e < 142u ? 141u : e);
+  inverse = __uint_as_float((e - 14u) << 23);
+  return __uint_as_float((127u + 14u + 127u - e) << 23);
 }
 
 // Multi-row inverse rotation H_d R_SO4^T u (unnormalised) of nvec rows in
@@ -130,6 +146,7 @@ struct TcCfg {
   static constexpr int PB = D * 3 / 8;
   static constexpr int ITEMS = kTcTok * (D / 32) / kTcThreads;   // 32-code groups per thread per tile
   static constexpr int Q_BYTES = kTcRows * D * 2;         // one of hi / lo
+  static constexpr int Q_TILE = 2 * Q_BYTES + kTcRows * 4;   // prepared: hi, lo, the rows' inverse scales
   static constexpr int KV_BYTES = kTcTok * D * 2;         // one K, K-residual or V tile
   static constexpr int NORM_BYTES = 2 * kTcTok * 4;       // s^K score_unit, s^V of one tile
   static constexpr int OFF_QLO = Q_BYTES;
@@ -330,13 +347,14 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     fail_s[0] = fail_s[1] = 0;
     mbar_fence_init();
   }
+  // kPfPrefix: hi and lo tile, then the rows' inverse scales.
+  const unsigned char *q_tile = a.q_tiles + (static_cast<long long>(kvh) * a.row_tiles + qt) * C::Q_TILE;
   if constexpr (PREFIX) {
     // The prepared query tiles; a wait that gives up counts as a product's.
     if (tid == 0) {
-      const unsigned char *src = a.q_tiles + (static_cast<long long>(kvh) * a.row_tiles + qt) * (2 * C::Q_BYTES);
       mbar_arrive_expect_tx(bar_q, 2 * C::Q_BYTES);
-      bulk_load(q_hi, src, C::Q_BYTES, bar_q);
-      bulk_load(q_lo, src + C::Q_BYTES, C::Q_BYTES, bar_q);
+      bulk_load(q_hi, q_tile, C::Q_BYTES, bar_q);
+      bulk_load(q_lo, q_tile + C::Q_BYTES, C::Q_BYTES, bar_q);
     }
   } else {
   // ---- prep, 32 rows per pass: rotate, split into float16 hi / lo (SW128 K-major) ----
@@ -356,9 +374,16 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     for (int i = tid; i < 32 * (D / 8); i += kTcThreads) {
       const int r = i / (D / 8), c = i % (D / 8), m = 32 * pass + r;
       uint32_t hv[4], lv[4];
+      float big = 0.f, back;   // over the row: D / 8 neighbouring lanes hold it
+#pragma unroll
+      for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(scratch[r * D + 8 * c + k]));
+#pragma unroll
+      for (int o = D / 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      const float sc = query_scale(big, back);
+      if (c == 0) nrm_s[m] = back;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float x0 = scratch[r * D + 8 * c + 2 * k], x1 = scratch[r * D + 8 * c + 2 * k + 1];
+        const float x0 = scratch[r * D + 8 * c + 2 * k] * sc, x1 = scratch[r * D + 8 * c + 2 * k + 1] * sc;
         const __half h0 = __float2half_rn(x0), h1 = __float2half_rn(x1);
         const __half l0 = __float2half_rn(x0 - __half2float(h0)), l1 = __float2half_rn(x1 - __half2float(h1));
         const __half2 hh = __halves2half2(h0, h1), ll = __halves2half2(l0, l1);
@@ -422,12 +447,19 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   bool failed = false;
   int qk_issued = 0, qk_done = 0, o_issued = 0, o_done = 0;
 
+  // The row's scores are those of its scaled query: times q_back.
+  float q_back;
   if constexpr (PREFIX) {
+    q_back = reinterpret_cast<const float *>(q_tile + 2 * C::Q_BYTES)[r];
     if (__syncthreads_or(!mbar_wait_bounded(bar_q, 0))) {
       failed = true;
       n_tiles = 0;
     }
+  } else {
+    q_back = nrm_s[r];
+    __syncthreads();   // the norms go over it
   }
+  const bool q_scaled = __any_sync(0xffffffffu, q_back != 1.f);
   if (n_tiles > 0) {
     store_norm();
     if (n_tiles > 1) fetch_norm(1);
@@ -481,6 +513,10 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
         f2_unpack(f2_mul(f2_pack(v[4 * k], v[4 * k + 1]), n.x), x[16 * c + 4 * k], x[16 * c + 4 * k + 1]);
         f2_unpack(f2_mul(f2_pack(v[4 * k + 2], v[4 * k + 3]), n.y), x[16 * c + 4 * k + 2], x[16 * c + 4 * k + 3]);
       }
+    }
+    if (q_scaled) {
+#pragma unroll
+      for (int j = 0; j < HC; ++j) x[j] *= q_back;
     }
     if (t0 + kTcTok - 1 > pw_min || t0 + kTcTok > tend) {   // uniform over the warp pair
 #pragma unroll

@@ -4,8 +4,9 @@
 // arguments, tables and tile layouts it shares.
 //
 // The mathematics is prefill.cuh's: S = Q~hi K~hi^T + Q~lo K~hi^T + Q~hi K~lo^T
-// with float16 hi and lo parts of the rotated query and of the centroids,
-// x = S s^K scale, p = 2^(x - r), O += P_hi V~ + P_lo V~ with P = p s^V.
+// with float16 hi and lo parts of the rotated query (each row scaled by a power
+// of two: query_scale) and of the centroids, x = S s^K scale, p = 2^(x - r),
+// O += P_hi V~ + P_lo V~ with P = p s^V.
 //
 // Why the queries sit in tensor memory: with both operands in shared memory a
 // 128 x 128 x 16 product reads 8 KB in its 64 cycles, all that shared memory
@@ -54,6 +55,7 @@
 constexpr int kRowsWarps = 16, kRowsUnpackWarps = 7;
 constexpr int kRowsThreads = 32 * kRowsWarps;
 constexpr int kRowsTok = 128;
+static_assert(kTcRows / kRowsWarps == 8, "rows of a warp: a byte of flags each");
 constexpr float kRowsHeadroom = 8.f;   // log2: how far the reference is set above the score that moves it
 
 struct RowsCfg {
@@ -63,7 +65,8 @@ struct RowsCfg {
   static constexpr int OFF_NORM = 2 * STAGE;               // [4][s^K unit, s^V][128] float32
   static constexpr int OFF_XCHG = OFF_NORM + 4 * 2 * kRowsTok * 4;   // [2][2][128] float32
   static constexpr int OFF_BAR = OFF_XCHG + 2 * 2 * kTcRows * 4;
-  static constexpr int SMEM = OFF_BAR + 24 * 8;
+  static constexpr int OFF_BACK = OFF_BAR + 24 * 8;        // [128] float32, the rows' inverse query scales
+  static constexpr int SMEM = OFF_BACK + kTcRows * 4;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
@@ -110,6 +113,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   float *norms = reinterpret_cast<float *>(smem + C::OFF_NORM);
   float *xchg = reinterpret_cast<float *>(smem + C::OFF_XCHG);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+  float *q_back = reinterpret_cast<float *>(smem + C::OFF_BACK);
   uint64_t *k_full = bars /* [2] */, *v_full = bars + 2 /* [2] */, *k_free = bars + 4 /* [2] */,
            *v_free = bars + 6 /* [2] */, *s_full = bars + 8 /* [2] */, *p_full = bars + 10 /* [2] */,
            *n_full = bars + 12 /* [4] */, *o_done = bars + 16, *all_done = bars + 17;
@@ -215,8 +219,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   {
     const float *prm = a.params_k + static_cast<size_t>(kvh) * 256 + 8 * lane;
     const Quat ql = load_quat(prm), qr = load_quat(prm + 4);
-    for (int i = warp; i < kTcRows; i += kRowsWarps) {
-      const long long row = query_of(i);
+    auto rotated = [&](long long row) {
       float x[4] = {0.f, 0.f, 0.f, 0.f};
       if (row >= 0) {
         const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const __half *>(a.q) + row * 128 + 4 * lane);
@@ -239,7 +242,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
         for (int e = 0; e < 4; ++e) x[e] = fmaf(x[e], sgn, __shfl_xor_sync(0xffffffffu, x[e], lm));
       }
       const Quat v{x[0] * inv_sqrt_d, x[1] * inv_sqrt_d, x[2] * inv_sqrt_d, x[3] * inv_sqrt_d};
-      const Quat y = block_forward(ql, qr, v, FULL);
+      return block_forward(ql, qr, v, FULL);
+    };
+    auto stage = [&](int i, const Quat &y) {
       const __half2 h0 = __floats2half2_rn(y.w, y.x), h1 = __floats2half2_rn(y.y, y.z);
       const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
       unsigned char *at = smem + 256 * i + 16 * ((lane >> 1) ^ (i & 15)) + 8 * (lane & 1);
@@ -247,6 +252,30 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
           make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
       *reinterpret_cast<uint2 *>(at + 256 * kTcRows) =
           make_uint2(pack_f16x2(y.w - f0.x, y.x - f0.y), pack_f16x2(y.y - f1.x, y.z - f1.y));
+    };
+    auto largest = [](const Quat &y) { return fmaxf(fmaxf(fabsf(y.w), fabsf(y.x)), fmaxf(fabsf(y.y), fabsf(y.z))); };
+    // Bit k: row k of the warp has a component of 1/4 or more (or no query),
+    // bit 8 + k: one of 2^15 or more.  Rows that need a scale are done again
+    // (a maximum over the warp in every row's chain cost 1.3 us of a CTA).
+    uint32_t range = 0;
+    for (int i = warp, k = 0; i < kTcRows; i += kRowsWarps, ++k) {
+      const long long row = query_of(i);
+      const Quat y = rotated(row);
+      const float big = largest(y);
+      range |= (row < 0 || big >= 0.25f ? 1u : 0u) << k | (big >= 32768.f ? 256u : 0u) << k;
+      stage(i, y);
+    }
+    range = __reduce_or_sync(0xffffffffu, range);
+    if (lane < kTcRows / kRowsWarps) q_back[warp + kRowsWarps * lane] = 1.f;
+    __syncwarp();
+#pragma unroll 1
+    for (uint32_t redo = (~range & 255u) | range >> 8; redo; redo &= redo - 1) {
+      const int i = warp + kRowsWarps * (__ffs(redo) - 1);
+      const Quat y = rotated(query_of(i));
+      float back;   // (not negative: the maximum is ordered as integers)
+      const float sc = query_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(largest(y)))), back);
+      stage(i, Quat{y.w * sc, y.x * sc, y.y * sc, y.z * sc});
+      if (lane == 0) q_back[i] = back;
     }
   }
   tc_fence_before();
@@ -295,8 +324,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
       n_sink = a.n_sink;
     }
     const int last = p_row < tend - 1 ? p_row : tend - 1;
+    const float back = q_back[i];   // the row's scores are those of its scaled query: times back
     float ref = -INFINITY;
     uint64_t la = f2_pack(0.f, 0.f), lb = la;
+    auto tiles = [&](auto scaled) {
+    constexpr bool SCALED = decltype(scaled)::value;
     for (int j = 0; j < n_iter; ++j) {
       // (After a wait that gave up the loop goes on without waiting, so that
       // the barriers of a pair of warps always meet.)
@@ -330,6 +362,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
           const ulonglong2 n = n4[k];
           f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c][4 * k]), __uint_as_float(s[c][4 * k + 1])), n.x), x[c][4 * k], x[c][4 * k + 1]);
           f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c][4 * k + 2]), __uint_as_float(s[c][4 * k + 3])), n.y), x[c][4 * k + 2], x[c][4 * k + 3]);
+        }
+        if constexpr (SCALED) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[c][e] *= back;
         }
         if (part) {
 #pragma unroll
@@ -402,6 +438,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + (j & 1));
     }
+    };
+    // Two versions of the loop: the factor (or a branch around it) in the one
+    // that hardly a call needs it in costs 1.3 % of the windowed prefill.
+    if (__any_sync(0xffffffffu, back != 1.f))
+      tiles(std::true_type{});
+    else
+      tiles(std::false_type{});
     // ---- the row's result ----
     if (ok && n_iter > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(all_done, 0));
     if (!ok) atomicOr(&g_decode_error, kErrWaitTimeout);

@@ -4,11 +4,12 @@
 // rows.  Included by isoq_serve.cu inside namespace isoq::decode.
 
 // Query rows in the operand layout: row r of KV head kvh is rotated (the order
-// of prep_i8_kernel), split into float16 hi and lo parts and written to its
-// 128-row tile, 128B-swizzled K-major; rows past the batch are zeros.  One
-// warp per row.
+// of prep_i8_kernel), scaled (query_scale), split into float16 hi and lo parts
+// and written to its 128-row tile, 128B-swizzled K-major, its inverse scale
+// behind the two; rows past the batch are zeros.  One warp per row.
 template <int D, bool FULL>
 __global__ void __launch_bounds__(128) prep_prefix_kernel(const SplitArgs a, unsigned char *tiles, int row_tiles) {
+  using C = TcCfg<D>;
   constexpr int E = D / 32, QBLK = kTcRows * 128;
   const int r = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5), kvh = blockIdx.y, lane = threadIdx.x & 31;
   float x[E];
@@ -44,13 +45,24 @@ __global__ void __launch_bounds__(128) prep_prefix_kernel(const SplitArgs a, uns
   const float inv = rsqrtf(static_cast<float>(D));
   const float *prm = a.params_k + static_cast<size_t>(kvh) * 2 * D;
   const int m = r % kTcRows;
-  unsigned char *hi = tiles + (static_cast<long long>(kvh) * row_tiles + r / kTcRows) * (4 * kTcRows * D);
-  unsigned char *lo = hi + 2 * kTcRows * D;
+  unsigned char *hi = tiles + (static_cast<long long>(kvh) * row_tiles + r / kTcRows) * C::Q_TILE;
+  unsigned char *lo = hi + C::Q_BYTES;
+  Quat rot[E / 4];
+  float big = 0.f, back;
 #pragma unroll
   for (int u = 0; u < E / 4; ++u) {
     const int bi = (E / 4) * lane + u;
     const Quat v{x[4 * u] * inv, x[4 * u + 1] * inv, x[4 * u + 2] * inv, x[4 * u + 3] * inv};
-    const Quat y = block_forward(load_quat(prm + 8 * bi), load_quat(prm + 8 * bi + 4), v, FULL);
+    rot[u] = block_forward(load_quat(prm + 8 * bi), load_quat(prm + 8 * bi + 4), v, FULL);
+    big = fmaxf(fmaxf(fmaxf(big, fabsf(rot[u].w)), fabsf(rot[u].x)), fmaxf(fabsf(rot[u].y), fabsf(rot[u].z)));
+  }
+  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));   // (not negative: ordered as integers)
+  const float sc = query_scale(big, back);
+  if (lane == 0) reinterpret_cast<float *>(hi + 2 * C::Q_BYTES)[m] = back;
+#pragma unroll
+  for (int u = 0; u < E / 4; ++u) {
+    const int bi = (E / 4) * lane + u;
+    const Quat y{rot[u].w * sc, rot[u].x * sc, rot[u].y * sc, rot[u].z * sc};
     const __half2 h0 = __floats2half2_rn(y.w, y.x), h1 = __floats2half2_rn(y.y, y.z);
     const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
     const uint32_t off = tc_off(m, 4 * bi, QBLK);

@@ -87,3 +87,57 @@ def test_pages_that_no_query_sees_are_not_followed(dtype, d, bits, hq, hkv, p):
                                                max_len=max_len, window=window, n_sink=n_sink)
         ref = S.paged_decode(q[rows], pages, table[rows], lens[rows], *par, bits, 0, scale, max_len, window, n_sink)
         _check(got, ref, dtype, q, pages[2], pages[3], scale)
+
+
+def _queries(g, shape, kind):
+    """float16 queries and the scale that keeps their scores moderate.
+    "large": rows of +-60,000 in a Walsh-Hadamard pattern, whose transform
+    gathers in one coordinate (far above 65,504 once rotated), and random
+    signs of it; "tiny": float16's subnormal numbers; "mixed": large, ordinary
+    and tiny rows in turn (a large row's scores are far apart)."""
+    d = shape[-1]
+    rows = int(np.prod(shape[:-1]))
+    q = g.standard_normal((rows, d))
+    if kind == "tiny":
+        return (q * 4e-7).astype(F16).reshape(shape), 1 / (4e-7 * np.sqrt(d))
+    had = np.array([[1.0]])
+    while had.shape[0] < d:
+        had = np.block([[had, had], [had, -had]])
+    big = 60000 * had[g.integers(0, d, rows)] * np.where(g.random((rows, 1)) < 0.5, 1, g.choice([-1, 1], (rows, d)))
+    if kind == "large":
+        return big.astype(F16).reshape(shape), 1 / (60000 * np.sqrt(d))
+    turn = np.arange(rows)[:, None] % 3
+    return np.where(turn == 0, big, np.where(turn == 1, q, 4e-7 * q)).astype(F16).reshape(shape), 1 / np.sqrt(d)
+
+
+@pytest.mark.parametrize("kind", ["large", "tiny", "mixed"])
+@pytest.mark.parametrize("d,rows", [(128, 8), (128, 9), (128, 130), (256, 23), (256, 24), (256, 130)])
+def test_prefix_of_any_query_magnitude(d, rows, kind):
+    """Rows just below and above the ones that take the tcgen05 split."""
+    g = np.random.default_rng(rows)
+    tp, tmax = 700, 40
+    prefix, cache = _cache(g, (1, tp), d, 3), _cache(g, (rows, 1, tmax), d, 3)
+    par = _params(1, d, 0)
+    q, scale = _queries(g, (rows, 1, d), kind)
+    lens, plen = g.integers(0, tmax + 1, rows).astype(np.int32), np.array([tp - 3], np.int32)
+    got = isoq.isoq_decode_attention_prefix(_t(q), *map(_t, prefix), _t(plen), *map(_t, cache), _t(lens), *map(_t, par), 3,
+                                            0, scale=scale)
+    some = sorted(set(range(min(rows, 24))) | {rows - 1})
+    ref = S.prefix_decode(q[some], prefix, tp - 3, *[c[some] for c in cache], lens[some], *par, 3, 0, scale)
+    _check(got[some], ref, F16, q, cache[2], cache[3], scale)
+
+
+@pytest.mark.parametrize("kind", ["large", "tiny", "mixed"])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 2), (128, 8, 1), (256, 2, 2), (256, 8, 1)])
+def test_prefill_of_any_query_magnitude(d, hq, hkv, kind):
+    """The windowed and the plain chunk; both at d = 128 and 256."""
+    g = np.random.default_rng(d + hq)
+    tmax, tq = 320, 24
+    lens = np.array([300, 24], np.int32)
+    cache, par = _cache(g, (2, hkv, tmax), d, 3), _params(hkv, d, 0)
+    q, scale = _queries(g, (2, tq, hq, d), kind)
+    args = (*map(_t, cache), _t(lens), *map(_t, par), 3, 0)
+    for window, n_sink, call in [(150, 20, lambda: isoq.isoq_prefill_attention_window(_t(q), *args, 150, 20, scale=scale)),
+                                 (1 << 30, 0, lambda: isoq.isoq_prefill_attention(_t(q), *args, scale=scale))]:
+        ref = S.window_prefill(q, *cache, lens, *par, 3, 0, scale, window, n_sink)
+        _check(call(), ref, F16, q, cache[2], cache[3], scale)
