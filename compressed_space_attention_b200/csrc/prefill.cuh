@@ -27,7 +27,8 @@
 //   each thread reads its half row of S(j) (tcgen05.ld), scales it by
 //   s^K scale / alpha, masks it on diagonal tiles, exchanges its half-row
 //   maximum with the partner warp through the consumed S buffer, writes
-//   P = p s^V as float16 hi and lo parts (22 bits of each weight) over that
+//   P = p s^V as float16 hi and lo parts (22 bits of each weight, s^V scaled by
+//   a power of two for the whole CTA: value_scale) over that
 //   S buffer in TMEM and, when its warp's maximum moved, rescales its half
 //   of the O row in TMEM; the CTA expands V tile j into its own tile buffer
 //   and one thread issues O += P_hi V~ + P_lo V~ (A = P from tensor memory,
@@ -105,6 +106,33 @@ __device__ __forceinline__ float query_scale(float mx, float &inverse) {
   uint32_t e = __float_as_uint(mx) >> 23;
   e = e < 64u ? 64u : (e >= 125u && e < 142u ? 141u : e);
   inverse = __uint_as_float((e - 14u) << 23);
+  return __uint_as_float((127u + 14u + 127u - e) << 23);
+}
+
+// The largest finite V norm (float16 bits) of tokens [a, b), over the lanes of a
+// warp; 0 if there is none.  Eight loads are under way at once: the pass
+// stands before a CTA's first tile.
+template <int THREADS>
+__device__ __forceinline__ uint32_t largest_norm(const uint16_t *norms, int a, int b, int tid) {
+  uint32_t mx = 0;
+  for (int t = a; t < b; t += 8 * THREADS) {
+    uint32_t u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = b - t > k * THREADS + tid ? __ldg(norms + t + k * THREADS + tid) & 0x7FFFu : 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = u[k] < 0x7C00u && u[k] > mx ? u[k] : mx;   // magnitudes order as integers
+  }
+  return __reduce_max_sync(0xffffffffu, mx);
+}
+
+// The scale of V's norms for the float16 hi and lo parts of the weights p s^V
+// (p <= 1): the power of two that takes the largest of them (float16 bits) to
+// [2^14, 2^15).  Unscaled, weights below 2^-14 lose bits and those below 2^-25
+// vanish, however many there are of them; with it, that is relative to the
+// largest norm.  The results are divided by it.
+__device__ __forceinline__ float value_scale(uint32_t largest) {
+  if (largest == 0) return 1.f;
+  const uint32_t e = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(largest)))) >> 23;
   return __uint_as_float((127u + 14u + 127u - e) << 23);
 }
 
@@ -293,10 +321,10 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     n_tiles = (tend - t_base + kTcTok - 1) / kTcTok;
   }
   // WIN: tiles [0, n_sink_tiles), then from win_tile on.
-  int n_sink_tiles = 0, win_tile = 0;
+  int n_sink_tiles = 0, win_tile = 0, sink = 0, lo = 0;
   if constexpr (WIN) {
-    const int sink = a.n_sink < tend ? a.n_sink : tend;
-    int lo = p_first >= a.window ? p_first - a.window + 1 : 0;   // the first row's window begins here
+    sink = a.n_sink < tend ? a.n_sink : tend;
+    lo = p_first >= a.window ? p_first - a.window + 1 : 0;   // the first row's window begins here
     if (lo > tend) lo = tend;
     if (lo > sink) {
       const int all = n_tiles;
@@ -334,6 +362,15 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     fetch_norm(0);
   }
 
+  // One word per warp where the first V tile goes later.
+  uint32_t *v_max = reinterpret_cast<uint32_t *>(vt);
+  {
+    // What no row sees has no part in the scale: with a gap behind the sinks,
+    // tokens [0, sink) and from lo on.
+    const uint32_t m0 = lo > sink ? largest_norm<kTcThreads>(nvb, 0, sink, tid) : 0u;
+    const uint32_t m1 = largest_norm<kTcThreads>(nvb, lo > sink ? lo : t_base, tend, tid);
+    if ((tid & 31) == 0) v_max[warp] = m0 > m1 ? m0 : m1;
+  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(C::TMEM_COLS));
@@ -399,6 +436,10 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  uint32_t norm_max = 0;
+#pragma unroll
+  for (int w = 0; w < kTcThreads / 32; ++w) norm_max = v_max[w] > norm_max ? v_max[w] : norm_max;
+  const float v_scale = value_scale(norm_max);
   const uint32_t tmem = *tmem_slot;
   const uint32_t t_o = tmem + 128;                           // S buffers at columns [0, 64), [64, 128); O after
   // Warp w reads TMEM lanes 32 (w % 4) .. + 31 (its sub-partition) and
@@ -412,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   // product into S buffer j % 2.  The caller has made sure the K tile and
   // that S buffer are free.
   auto store_norm = [&]() {
-    if (tid < 2 * kTcTok) nrm_s[tid] = __half2float(__ushort_as_half(nrm)) * (tid < kTcTok ? a.score_unit : 1.f);
+    if (tid < 2 * kTcTok) nrm_s[tid] = __half2float(__ushort_as_half(nrm)) * (tid < kTcTok ? a.score_unit : v_scale);
   };
   auto stage_qk = [&](int j) {
     tc_expand<D, true>(kc, kt, klt, a, tid);
@@ -459,7 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     q_back = nrm_s[r];
     __syncthreads();   // the norms go over it
   }
-  const bool q_scaled = __any_sync(0xffffffffu, q_back != 1.f);
+  const uint64_t back2 = f2_pack(q_back, q_back);
   if (n_tiles > 0) {
     store_norm();
     if (n_tiles > 1) fetch_norm(1);
@@ -514,10 +555,6 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
         f2_unpack(f2_mul(f2_pack(v[4 * k + 2], v[4 * k + 3]), n.y), x[16 * c + 4 * k + 2], x[16 * c + 4 * k + 3]);
       }
     }
-    if (q_scaled) {
-#pragma unroll
-      for (int j = 0; j < HC; ++j) x[j] *= q_back;
-    }
     if (t0 + kTcTok - 1 > pw_min || t0 + kTcTok > tend) {   // uniform over the warp pair
 #pragma unroll
       for (int j = 0; j < HC; ++j)
@@ -562,12 +599,12 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     tc_fence_after();
     tmx = fmaxf(tmx, __uint_as_float(tc_ld1(s_col + 16 + 16 * (half ^ 1))));
     tc_wait_ld();
-    const float nm = fmaxf(mx, tmx);
+    const float nm = fmaxf(mx, tmx * q_back);
     const float base = nm == -INFINITY ? 0.f : nm;
     const float f = ex2f(mx - base);                            // 0 while mx = -inf
     const bool moved = __any_sync(0xffffffffu, nm > mx);       // the same in both warps of the pair
     mx = nm;
-    const uint64_t base2 = f2_pack(base, base);
+    const uint64_t base2 = f2_pack(-base, -base);
     l2 = f2_mul(l2, f2_pack(f, f));
     // P = p s^V as float16 hi and lo parts: tokens 2i, 2i + 1 of the tile in
     // column i of the hi block (columns 0..31) and of the lo block (32..63).
@@ -578,7 +615,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
       for (int k = 0; k < 4; ++k) {
         const int j = 8 * c + 2 * k;
         float p0, p1;
-        f2_unpack(f2_sub(f2_pack(x[j], x[j + 1]), base2), p0, p1);
+        f2_unpack(f2_fma(f2_pack(x[j], x[j + 1]), back2, base2), p0, p1);
         const uint64_t p2 = f2_pack(ex2f(p0), ex2f(p1));
         l2 = f2_add(l2, p2);
         const ulonglong2 n = nv4[j >> 2];
@@ -666,6 +703,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     const bool live = row < a.batch * a.group;
     const long long query = live ? static_cast<long long>(row / a.group) * a.hq + kvh * a.group + row % a.group : 0;
     const long long slot = query * a.slot_stride + b;
+    const float unit = a.acc_unit / v_scale;
 #pragma unroll 1
     for (int c = 0; c < OH / 16; ++c) {
       float v[16];
@@ -679,8 +717,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
         float4 *dst = reinterpret_cast<float4 *>(a.ws_acc + slot * D + OH * half + 16 * c);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          dst[j] = make_float4(v[4 * j] * a.acc_unit, v[4 * j + 1] * a.acc_unit, v[4 * j + 2] * a.acc_unit,
-                               v[4 * j + 3] * a.acc_unit);
+          dst[j] = make_float4(v[4 * j] * unit, v[4 * j + 1] * unit, v[4 * j + 2] * unit, v[4 * j + 3] * unit);
       }
     }
     if (live && half == 0)
@@ -696,7 +733,7 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
     xchg[half * kTcRows + r] = l;
     __syncthreads();
     const float lt = l + xchg[(half ^ 1) * kTcRows + r];
-    const float inv = lt > 0.f ? a.out_unit / lt : 0.f;
+    const float inv = lt > 0.f ? a.out_unit / lt / v_scale : 0.f;
     for (int pass = 0; pass < kTcRows / 32; ++pass) {
       __syncthreads();   // scratch (over the K and V tiles) is free
       if (sub == pass) {

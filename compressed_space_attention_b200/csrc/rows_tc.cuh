@@ -22,10 +22,9 @@
 //               weights go over the scores (per 32 tokens 16 columns of hi
 //               and 16 of lo parts).  The reference r moves only when a score
 //               passes it, and then to that score + 8: p <= 1 always, and O,
-//               which follows, is seldom rescaled.  s^V is scaled by the power
-//               of two that takes the largest one of the CTA's tokens to about
-//               2^15, so P stays far from float16's subnormal numbers for all
-//               that headroom.
+//               which follows, is seldom rescaled.  s^V is scaled by a power
+//               of two (value_scale), so P stays far from float16's subnormal
+//               numbers for all that headroom.
 //   warps 8-14  unpack: codes (fetched one tile ahead into registers) to
 //               float16 centroids and residuals of K, centroids of V, and the
 //               norms.
@@ -132,15 +131,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   const int tq0 = WIN ? qt * per_cta : 0;
   const int p_first = WIN ? *lens - a.tq + tq0 : 0;          // position of the CTA's first row
   const int total_rows = WIN ? 0 : a.batch * G;
-  int tend, t_base = 0, n_sink_tiles = 0, win_tile = 0, n_iter, j_base = 0;
+  int tend, t_base = 0, n_sink_tiles = 0, win_tile = 0, sink = 0, lo = 0, n_iter, j_base = 0;
   if constexpr (WIN) {
     int p_last = p_first + per_cta - 1;
     if (tq0 + per_cta > a.tq) p_last = *lens - 1;
     tend = p_last + 1 < len ? p_last + 1 : len;
     if (tend < 0) tend = 0;
     const int all = (tend + kRowsTok - 1) / kRowsTok;
-    const int sink = a.n_sink < tend ? a.n_sink : tend;
-    int lo = p_first >= a.window ? p_first - a.window + 1 : 0;
+    sink = a.n_sink < tend ? a.n_sink : tend;
+    lo = p_first >= a.window ? p_first - a.window + 1 : 0;
     if (lo > tend) lo = tend;
     n_iter = all;
     if (lo > sink) {
@@ -179,19 +178,26 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   };
   const long long cache0 = WIN ? (static_cast<long long>(b) * a.hkv + kvh) * a.tmax : kvh * a.head_stride;
 
-  // The largest finite V norm of the tokens that the CTA reads.
   {
-    float mx = 0.f;
-    for (int j = tid >> 7; j < n_iter; j += kRowsThreads / 128) {
-      const int tok = tile_t0(j) + (tid & (kRowsTok - 1));
-      if (tok < tend) {
-        const float v = __half2float(__ushort_as_half(__ldg(a.norms_v + cache0 + tok)));
-        mx = v <= 65504.f ? fmaxf(mx, v) : mx;
+    uint32_t mx = 0;
+    auto among = [&](int t0, int t1) {
+      const uint32_t u = largest_norm<kRowsThreads>(a.norms_v + cache0, t0, t1, tid);
+      mx = u > mx ? u : mx;
+    };
+    if constexpr (WIN) {
+      // Of the CTA's tiles (n0 of sinks, then the others) the tokens that some
+      // row sees: with a gap behind the sinks, those before `sink` or from lo on.
+      const int n0 = max(min(n_sink_tiles - j_base, n_iter), 0);
+      const int a0 = kRowsTok * j_base, b0 = a0 + kRowsTok * n0, a1 = tile_t0(n0), b1 = min(a1 + kRowsTok * (n_iter - n0), tend);
+      if (n0 > 0) {
+        among(a0, min(b0, sink));
+        among(max(a0, lo), min(b0, tend));
       }
+      among(lo > sink ? max(a1, lo) : a1, b1);
+    } else {
+      among(t_base, tend);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) xchg[warp] = mx;
+    if (lane == 0) reinterpret_cast<uint32_t *>(xchg)[warp] = mx;
   }
   if (warp == kRowsWarps - 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512));
@@ -284,13 +290,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
   const uint32_t tmem = *tmem_slot;
   const uint32_t t_o = tmem + 256, t_q = tmem + 384;       // Q~hi 64 columns, Q~lo 64
   const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-  float v_scale = 1.f;     // a power of two; the results are divided by it
-  {
-    float mx = 0.f;
+  uint32_t norm_max = 0;
 #pragma unroll
-    for (int w = 0; w < kRowsWarps; ++w) mx = fmaxf(mx, xchg[w]);
-    if (mx > 0.f) v_scale = __uint_as_float(static_cast<uint32_t>(127 + 14 + 127 - (__float_as_uint(mx) >> 23)) << 23);
+  for (int w = 0; w < kRowsWarps; ++w) {
+    const uint32_t u = reinterpret_cast<const uint32_t *>(xchg)[w];
+    norm_max = u > norm_max ? u : norm_max;
   }
+  const float v_scale = value_scale(norm_max);
   if (warp < 8) {   // warps 0-3 the hi parts, 4-7 the lo parts
     const int i = 32 * (warp & 3) + lane, part = warp >> 2;
 #pragma unroll 1

@@ -8,6 +8,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import compressed_space_attention_b200 as isoq  # noqa: E402
+import oracle as O  # noqa: E402
+from isoq_testlib import f16_half_ulp  # noqa: E402
 from oracle import serving as S  # noqa: E402
 from test_parity_serving import DEV, F16, F32, _cache, _check, _pages, _params, _t  # noqa: E402
 
@@ -141,3 +143,68 @@ def test_prefill_of_any_query_magnitude(d, hq, hkv, kind):
                                  (1 << 30, 0, lambda: isoq.isoq_prefill_attention(_t(q), *args, scale=scale))]:
         ref = S.window_prefill(q, *cache, lens, *par, 3, 0, scale, window, n_sink)
         _check(call(), ref, F16, q, cache[2], cache[3], scale)
+
+
+@pytest.mark.parametrize("v_norm,hidden", [(1e-4, 1e-4), (1e-4, 65504.0), (0.01, 65504.0), (3.0, 3.0), (30000.0, 1e-7)])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("form", ["prefix", "window", "plain"])
+def test_many_small_weights_count_whatever_the_v_norms(form, d, v_norm, hidden):
+    """One token's score is 12 (log2) above those of 8,191 others, and all have
+    one V vector, which therefore is the output: it misses what a form loses of
+    the 8,191 weights of 2^-12 (2/3 of the sum).  Norms that unscaled float16
+    weights cannot hold; behind the window, norms that no query sees, other
+    than the seen ones.  Tolerance: half a float16 step of the value, and
+    2^-15 of the V vector (its length is v_norm) for the float16 centroids
+    (1.9e-5 relative) and the float32 sums."""
+    g = np.random.default_rng(d)
+    n, t = 8192, 8192 + (200 if form == "window" else 0)
+    par = _params(1, d, 0)
+    one = _cache(g, (1, 1), d, 3)
+    k, v = (np.repeat(x, t, axis=1) for x in one[:2])
+    nk, nv = np.full((1, t), 8.0, F16), np.full((1, t), v_norm, F16)
+    nv[:, :t - n] = hidden
+    top = t - n + 40
+    nk[:, top] = 16.0
+    q1 = g.standard_normal(d).astype(F16)
+    unit_k, unit_v = (O.dequantize(x[:, :1], np.ones((1, 1), F16), p, 3, 0, d)[0, 0] for x, p in zip((k, v), par))
+    unit = float(q1.astype(np.float64) @ unit_k)
+    scale = 12 * np.log(2) / (8 * unit)
+    args = (*map(_t, par), 3, 0)
+    if form == "prefix":
+        rows = 9 if d == 128 else 24
+        q = np.tile(q1, (rows, 1, 1))
+        own = _cache(g, (rows, 1, 8), d, 3)
+        got = isoq.isoq_decode_attention_prefix(_t(q), _t(k), _t(v), _t(nk), _t(nv), _t(np.array([t], np.int32)),
+                                                *map(_t, own), _t(np.zeros(rows, np.int32)), *args, scale=scale)
+    else:
+        q = q1.reshape(1, 1, 1, d)
+        cache = [_t(x[None]) for x in (k, v, nk, nv)]
+        lens = _t(np.array([t], np.int32))
+        got = isoq.isoq_prefill_attention(_t(q), *cache, lens, *args, scale=scale) if form == "plain" else \
+            isoq.isoq_prefill_attention_window(_t(q), *cache, lens, *args, n, 0, scale=scale)
+    assert isoq.isoq_check_device_error() == 0
+    ref = float(F16(v_norm)) * unit_v
+    err = np.abs(got.cpu().numpy().astype(np.float64).reshape(-1, d) - ref)
+    assert (err <= f16_half_ulp(ref) + 2.0 ** -15 * float(F16(v_norm))).all(), (err.max(), np.abs(ref).max())
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("tmax,window,n_sink", [(504, 400, 5), (504, 300, 200), (3000, 900, 700), (3000, 2200, 640), (504, 600, 3)])
+def test_v_norms_whose_largest_lies_anywhere(d, tmax, window, n_sink):
+    """The seen tokens' V norms are 2^-13 but for 32 tokens of 3: among the
+    sinks, where the window begins, in its last tokens; and 65,504 where no
+    query sees them.  A scale that left the 32 out would overflow."""
+    g = np.random.default_rng(d + tmax)
+    cache, par = _cache(g, (1, 1, tmax), d, 3), _params(1, d, 0)
+    t, tq = tmax - 3, 2
+    q = g.standard_normal((1, tq, 1, d)).astype(F16)
+    lo = max(t - tq - window + 1, 0)
+    for at in (0, lo, max(lo, 128 * (lo // 128 + 1) - 32), t - 34):
+        nv = np.full((1, 1, tmax), 2.0 ** -13, F16)
+        nv[..., at:at + 32] = 3
+        seen = set(S.seen_tokens(t - 2, t, window, n_sink)) | set(S.seen_tokens(t - 1, t, window, n_sink))
+        nv[..., [j for j in range(tmax) if j not in seen]] = 65504
+        got = isoq.isoq_prefill_attention_window(_t(q), *map(_t, (*cache[:3], nv)), _t(np.array([t], np.int32)), *map(_t, par),
+                                                 3, 0, window, n_sink)
+        ref = S.window_prefill(q, *cache[:3], nv, [t], *par, 3, 0, 1 / np.sqrt(d), window, n_sink)
+        _check(got, ref, F16, q, cache[2], nv, 1 / np.sqrt(d))
