@@ -64,8 +64,9 @@ inline int row_share(int rows) { return static_cast<int>(div_up(rows, div_up(row
 // 128 tokens per split, 16.4 at 512).  Without a window the rows are taken to
 // fill three quarters of the longest, ragged as they are (16 rows of 8,192 to
 // 16,384 tokens, 8 KV heads: 121 us at 1,024 tokens per split, 134 at the 2,048
-// that full rows would suggest).  `slots`: CTAs resident per SM, 4 of the
-// integer split, 4, 2 or 1 of the CUDA-core one at d = 128, 256, 512.
+// that full rows would suggest).  `slots`: CTAs resident per SM (resident_ctas),
+// but 1 at d = 512, where a second CTA adds little (16 rows x 8,192 tokens, 8
+// heads, float32, 2 bits: 281 us with the chunk of 1, 302 with that of 2).
 template <int64_t C>
 inline void weigh_chunk(int64_t ctas, int64_t tokens, bool ragged, int64_t slots, int64_t &best_cost, int64_t &best_chunk) {
   constexpr int64_t kSms = 148, kCtaCost = 160;
@@ -106,10 +107,41 @@ struct DecodePlan {
   bool fused;                        // one launch of clusters, no workspace
 };
 
+// CTAs of the split that an SM holds, for `rows` query rows each: of the integer
+// split 4, but 3 for 8 rows at d = 128 and 4 rows at d = 256, 2 for 8 rows there;
+// of the CUDA-core one 4 at d = 128, 2 or 3 at 256, 1 or 2 at 512.  Measured
+// against 4 for every integer split and every cluster, and 2 of the CUDA-core
+// one at d = 256: 32 rows x 1,024 tokens, 32 query over 4 KV heads, float16, d =
+// 256: 49.3 -> 36.5 us, d = 128: 30.1 -> 25.1; 16 x 512 tokens, 16 over 4,
+// float32, 4 bits, d = 512: 39.0 -> 28.9; 16 x 8,192 tokens, 16 over 4, float32,
+// 3 bits, d = 256: 149 -> 138; 16 x 12,288, 32 over 4, float16, d = 128: 77.2 ->
+// 75.1.
+template <int D, int BITS>
+constexpr int any_slots(int rows) {
+  return rows <= 2 ? AnyCfg<D, BITS, 2>::SLOTS : (rows <= 4 ? AnyCfg<D, BITS, 4>::SLOTS : AnyCfg<D, BITS, 8>::SLOTS);
+}
+
+template <int D>
+constexpr int any_slots_b(int bits, int rows) {
+  return bits == 2 ? any_slots<D, 2>(rows) : (bits == 3 ? any_slots<D, 3>(rows) : any_slots<D, 4>(rows));
+}
+
+template <int D>
+constexpr int i8_slots(int rows) {
+  return rows == 1   ? I8Cfg<D, 1>::MIN_BLOCKS
+         : rows == 2 ? I8Cfg<D, 2>::MIN_BLOCKS
+         : rows <= 4 ? I8Cfg<D, 4>::MIN_BLOCKS
+                     : I8Cfg<D, 8>::MIN_BLOCKS;
+}
+
+inline int resident_ctas(bool i8, int d, int bits, int rows) {
+  if (i8) return d == 128 ? i8_slots<128>(rows) : i8_slots<256>(rows);
+  return d == 128 ? any_slots_b<128>(bits, rows) : (d == 256 ? any_slots_b<256>(bits, rows) : any_slots_b<512>(bits, rows));
+}
+
 // Small problems run as one launch: up to 8 splits of a row group form a
 // cluster that merges its partial states itself.  Taken where 8 splits of at
-// most 16 blocks cover the longest list and all CTAs are resident at once (4 per
-// SM).  1 row, 32 query over 4 KV heads, 1,028 tokens: 12.3 us on the GPU
+// most 16 blocks cover the longest list and all CTAs are resident at once.  1 row, 32 query over 4 KV heads, 1,028 tokens: 12.3 us on the GPU
 // against 10.3 for the three launches, but 5.3 us of host time to queue it
 // against 9.9 (and no workspace): with the Python call around it a step of many
 // layers is bound by the queueing, 13.4 us a call against 19.2.
@@ -126,15 +158,18 @@ constexpr int prefix_tc_rows(int d) { return d == 128 ? 9 : 24; }
 
 // prefix_max < 0: no prefix.  The list of a row is cut into the same splits
 // whatever its length.
-DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int64_t window, int64_t n_sink,
-                       bool i8, bool prefix_tc = false) {
+DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int bits, int64_t window,
+                       int64_t n_sink, bool i8, bool prefix_tc = false) {
   DecodePlan p{};
-  const int G = Hq / Hkv, slots = i8 || d == 128 ? 4 : (d == 256 ? 2 : 1);
+  const int G = Hq / Hkv;
+  const int64_t rows = static_cast<int64_t>(B) * G;   // of a KV head, over the prefix
   p.share = row_share(G);
+  if (prefix_max >= 0) p.share_p = row_share(static_cast<int>(rows < 8 ? rows : 8));
+  const int slots = resident_ctas(i8, d, bits, !prefix_tc && p.share_p > p.share ? p.share_p : p.share);
   p.groups = static_cast<int>(div_up(G, p.share));
   const int64_t tokens = 32 * most_blocks(tmax, window, n_sink);
   if (prefix_max < 0) {
-    const int64_t ctas = static_cast<int64_t>(B) * Hkv * p.groups, blocks = tokens / 32, room = 4 * 148 / ctas;
+    const int64_t ctas = static_cast<int64_t>(B) * Hkv * p.groups, blocks = tokens / 32, room = slots * 148 / ctas;
     int64_t s = div_up(blocks, 4);
     if (s > kFusedSplits) s = kFusedSplits;
     if (s > room) s = room;
@@ -145,15 +180,14 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
       return p;
     }
   }
-  p.chunk = serve_chunk(static_cast<int64_t>(B) * Hkv * p.groups, tokens, window >= tmax, slots);
+  const int wave_slots = d == 512 ? 1 : slots;
+  p.chunk = serve_chunk(static_cast<int64_t>(B) * Hkv * p.groups, tokens, window >= tmax, wave_slots);
   p.splits = static_cast<int>(div_up(tokens, p.chunk));
   int64_t prep_rows = static_cast<int64_t>(B) * p.groups;
   if (prefix_max >= 0) {
-    const int64_t rows = static_cast<int64_t>(B) * G;
-    p.share_p = row_share(static_cast<int>(rows < 8 ? rows : 8));
     p.groups_p = static_cast<int>(div_up(rows, p.share_p));
     const int64_t tp = 32 * div_up(prefix_max, 32);
-    p.chunk_p = serve_chunk(static_cast<int64_t>(Hkv) * p.groups_p, tp > 0 ? tp : 32, false, slots);
+    p.chunk_p = serve_chunk(static_cast<int64_t>(Hkv) * p.groups_p, tp > 0 ? tp : 32, false, wave_slots);
     p.splits_p = static_cast<int>(div_up(tp, p.chunk_p));
     prep_rows += p.groups_p;
     if (prefix_tc) {
@@ -176,13 +210,21 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max,
   return p;
 }
 
-// The most that any of these shapes' plans needs (which one runs also depends
-// on types and alignment).
+// The most that any of these shapes' plans needs: which one runs also depends
+// on types, bits and alignment (the tcgen05 prefix has 3 bits).
 size_t most_workspace(int B, int Hq, int Hkv, int64_t tmax, int64_t prefix_max, int d, int64_t window, int64_t n_sink) {
   int64_t need = 0;
-  for (int k = 0; k < (prefix_max >= 0 ? 4 : 2); ++k) {
-    const DecodePlan p = plan_decode(B, Hq, Hkv, tmax, prefix_max, d, window, n_sink, k & 1, k & 2);
+  auto weigh = [&](int bits, bool i8, bool prefix_tc) {
+    const DecodePlan p = plan_decode(B, Hq, Hkv, tmax, prefix_max, d, bits, window, n_sink, i8, prefix_tc);
     need = p.acc_bytes + p.prep_bytes > need ? p.acc_bytes + p.prep_bytes : need;
+  };
+  for (int tc = 0; tc < (prefix_max >= 0 ? 2 : 1); ++tc) {
+    weigh(3, false, tc);
+    if (d != 512) weigh(3, true, tc);
+  }
+  if (d != 128) {   // (d = 128: as 3 bits)
+    weigh(2, false, false);
+    weigh(4, false, false);
   }
   return static_cast<size_t>(need);
 }
@@ -352,7 +394,7 @@ int isoq_decode_attention_window(const void *q_dev, int dtype, const uint8_t *pa
       !decode::aligned(norms_k_dev, 2) || !decode::aligned(norms_v_dev, 2) || !decode::aligned(seq_lens_dev, 4))
     return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
   const bool i8 = decode::i8_split(dtype, d, bits) && decode::i8_cache(norms_k_dev, norms_v_dev, Tmax);
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, -1, d, window, n_sink, i8);
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, -1, d, bits, window, n_sink, i8);
   st = decode::check_workspace(workspace_dev, workspace_bytes, decode::most_workspace(B, Hq, Hkv, Tmax, -1, d, window, n_sink));
   if (st) return st;
   decode::SplitArgs a{};
@@ -409,7 +451,7 @@ int isoq_decode_attention_prefix(const void *q_dev, int dtype, const uint8_t *pr
   const bool i8 = decode::i8_split(dtype, d, bits) && decode::i8_cache(norms_k_dev, norms_v_dev, Tmax) &&
                   (tc || (decode::i8_cache(prefix_norms_k_dev, prefix_norms_v_dev, prefix_head_stride) &&
                           prefix_tokens % 8 == 0));
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0, i8, tc);
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, Tmax, prefix_tokens, d, bits, Tmax, 0, i8, tc);
   st = decode::check_workspace(workspace_dev, workspace_bytes,
                                decode::most_workspace(B, Hq, Hkv, Tmax, prefix_tokens, d, Tmax, 0));
   if (st) return st;
@@ -465,7 +507,7 @@ int isoq_paged_decode_attention(const void *q_dev, int dtype, const uint8_t *pag
       !decode::aligned(block_table_dev, 4))
     return set_error(ISOQ_ERR_UNSUPPORTED, "misaligned pointer");
   const bool i8 = decode::i8_split(dtype, d, bits) && decode::i8_cache(norms_k_dev, norms_v_dev, 8);
-  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, max_len, -1, d, window, n_sink, i8);
+  const decode::DecodePlan p = decode::plan_decode(B, Hq, Hkv, max_len, -1, d, bits, window, n_sink, i8);
   st = decode::check_workspace(workspace_dev, workspace_bytes,
                                decode::most_workspace(B, Hq, Hkv, max_len, -1, d, window, n_sink));
   if (st) return st;

@@ -41,8 +41,12 @@ struct AnyCfg {
   static constexpr int OFF_W = OFF_Q + (D / 32) * Q_GROUP * 4;      // [warp][32][RG] weights
   static constexpr int OFF_TAB = OFF_W + kAnyWarps * 32 * RG * 4;   // [16] centroids
   static constexpr int OFF_ML = OFF_TAB + 16 * 4;           // [warp][RG] (m, l)
-  static constexpr int MIN_BLOCKS = D == 128 ? 4 : 1;       // by shared memory: 4, 2 and 1 at d = 128, 256, 512
+  static constexpr int MIN_BLOCKS = D == 128 ? 4 : 1;
   static constexpr int SMEM = OFF_ML + kAnyWarps * RG * 8;
+  // CTAs that an SM holds: by registers (128 a thread at d = 128, 168 at
+  // d = 256 up to 4 rows, up to 254 otherwise) and by shared memory.
+  static constexpr int BY_REGS = D == 128 ? 4 : (D == 256 && RG <= 4 ? 3 : 2), BY_SMEM = 233472 / (SMEM + 1024);
+  static constexpr int SLOTS = BY_REGS < BY_SMEM ? BY_REGS : BY_SMEM;
   static_assert(kAnyWarps * RG * D * 4 <= OFF_Q, "the warps' accumulators fit the stages");
 };
 

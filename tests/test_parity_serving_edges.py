@@ -208,3 +208,19 @@ def test_v_norms_whose_largest_lies_anywhere(d, tmax, window, n_sink):
                                                  3, 0, window, n_sink)
         ref = S.window_prefill(q, *cache[:3], nv, [t], *par, 3, 0, 1 / np.sqrt(d), window, n_sink)
         _check(got, ref, F16, q, cache[2], nv, 1 / np.sqrt(d))
+
+
+@pytest.mark.parametrize("dtype,d,bits,hq,hkv,b,t", [(F16, 256, 3, 32, 4, 32, 1024), (F16, 128, 3, 32, 4, 24, 1024),
+                                                     (F16, 256, 3, 16, 4, 32, 1000), (F32, 512, 4, 4, 4, 32, 1024),
+                                                     (F32, 512, 2, 8, 8, 16, 520), (F32, 256, 3, 16, 4, 16, 2048)])
+def test_decode_of_batches_that_fill_the_gpu(dtype, d, bits, hq, hkv, b, t):
+    """Batches next to what one resident wave of clusters takes, on both sides."""
+    g = np.random.default_rng(d + b)
+    cache, par = _cache(g, (b, hkv, t), d, bits), _params(hkv, d, 0)
+    lens = g.integers(1, t + 1, b).astype(np.int32)
+    lens[:3] = t, 1, 0
+    q = g.standard_normal((b, hq, d)).astype(dtype)
+    got = isoq.isoq_decode_attention_window(_t(q), *map(_t, cache), _t(lens), *map(_t, par), bits, 0, t)
+    rows = [0, 1, 2, 3, b // 2, b - 1]
+    ref = S.window_decode(q[rows], *[c[rows] for c in cache], lens[rows], *par, bits, 0, 1 / np.sqrt(d), t, 0)
+    _check(got[rows], ref, dtype, q, cache[2], cache[3], 1 / np.sqrt(d))
