@@ -533,16 +533,8 @@ int isoq_selftest_wait_timeout(uint64_t limit_ns, isoq_stream_t stream) {
   return ISOQ_OK;
 }
 
-__attribute__((visibility("hidden"))) int isoq_detail_take_decode_error(cudaStream_t stream, unsigned *out) {
-  unsigned zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, decode::g_decode_error, sizeof(unsigned), 0,
-                                            cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e == cudaSuccess && *out)
-    e = cudaMemcpyToSymbolAsync(decode::g_decode_error, &zero, sizeof(unsigned), 0,
-                                cudaMemcpyHostToDevice, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "error word: %s", cudaGetErrorString(e));
+__attribute__((visibility("hidden"))) cudaError_t isoq_detail_decode_error_word(void **word) {
+  return cudaGetSymbolAddress(word, decode::g_decode_error);
 }
 
 int isoq_decode_append(const void *k_new_dev, const void *v_new_dev, int dtype,

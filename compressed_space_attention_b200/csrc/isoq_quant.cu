@@ -1156,16 +1156,8 @@ int isoq_dequantize(const uint8_t *codes_dev, const uint16_t *norms_dev, int n_h
 }
 
 // Reads and clears this translation unit's device error word.
-__attribute__((visibility("hidden"))) int isoq_detail_take_quant_error(cudaStream_t stream, unsigned *out) {
-  unsigned zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, quant::g_quant_error, sizeof(unsigned), 0,
-                                            cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e == cudaSuccess && *out)
-    e = cudaMemcpyToSymbolAsync(quant::g_quant_error, &zero, sizeof(unsigned), 0,
-                                cudaMemcpyHostToDevice, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  return e == cudaSuccess ? ISOQ_OK : set_error(ISOQ_ERR_CUDA, "error word: %s", cudaGetErrorString(e));
+__attribute__((visibility("hidden"))) cudaError_t isoq_detail_quant_error_word(void **word) {
+  return cudaGetSymbolAddress(word, quant::g_quant_error);
 }
 
 }  // extern "C"

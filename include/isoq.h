@@ -514,14 +514,16 @@ int isoq_rotor_dequantize(const uint8_t *codes_dev, const uint16_t *norms_dev, i
                           int64_t head_stride, int64_t vec_stride, isoq_stream_t stream);
 
 /*
- * Reads and clears the current device's error word after synchronising
+ * Reads and clears the current device's error words after synchronising
  * `stream`.  Returns ISOQ_OK, ISOQ_ERR_TIMEOUT if a kernel's bounded wait
  * gave up since the last check (the kernel then stopped early and its
  * outputs are incomplete), ISOQ_ERR_INVALID_ARG if a decode append met a
  * row that already held Tmax tokens, a page index or slot was outside the
- * pages, or block tables had no room for a request, or ISOQ_ERR_CUDA (among others when
- * the prefill kernel found its dynamic shared memory off a 1024-byte
- * boundary and returned without output).
+ * pages, or block tables had no room for a request, or ISOQ_ERR_CUDA (among
+ * others when the prefill kernel found its dynamic shared memory off a
+ * 1024-byte boundary and returned without output).  Where several of them
+ * happened, the status is the first one's in this order, and isoq_last_error
+ * names them all.
  */
 int isoq_check_device_error(isoq_stream_t stream);
 

@@ -224,3 +224,28 @@ def test_decode_of_batches_that_fill_the_gpu(dtype, d, bits, hq, hkv, b, t):
     rows = [0, 1, 2, 3, b // 2, b - 1]
     ref = S.window_decode(q[rows], *[c[rows] for c in cache], lens[rows], *par, bits, 0, 1 / np.sqrt(d), t, 0)
     _check(got[rows], ref, dtype, q, cache[2], cache[3], 1 / np.sqrt(d))
+
+
+def test_every_error_since_the_last_check_is_named():
+    """A slot beyond the pages, a request without room and an append to a full
+    row before one check: one status, all three named, then nothing."""
+    g = np.random.default_rng(30)
+    par = [_t(x) for x in _params(1, 128, 0)]
+    pages, cache = [_t(x) for x in _cache(g, (2, 1, 16), 128, 3)], [_t(x) for x in _cache(g, (1, 1, 8), 128, 3)]
+    kv = _t(g.standard_normal((2, 1, 1, 128)).astype(F16))
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    bad_slot = lambda: isoq.isoq_paged_append(kv[0], kv[1], *pages, torch.tensor([32], device=DEV), *par, 3, 0)  # noqa: E731
+    no_room = lambda: isoq.isoq_build_block_tables(i32(0), i32(5), i32(), torch.zeros((1, 1), dtype=torch.int32, device=DEV), 16, 5)  # noqa: E731
+    full_row = lambda: isoq.isoq_decode_append(kv[0], kv[1], *cache, i32(8), *par, 3, 0)  # noqa: E731
+    said = {"slot outside the pages": bad_slot, "no room for a request": no_room, "held Tmax tokens": full_row}
+    assert isoq.isoq_check_device_error() == 0
+    for what, call in said.items():
+        call()
+        assert isoq.isoq_check_device_error() == isoq.ISOQ_ERR_INVALID_ARG
+        assert [w for w in said if w in isoq.last_error()] == [what]
+        assert isoq.isoq_check_device_error() == 0
+    for call in said.values():
+        call()
+    assert isoq.isoq_check_device_error() == isoq.ISOQ_ERR_INVALID_ARG
+    assert all(w in isoq.last_error() for w in said), isoq.last_error()
+    assert isoq.isoq_check_device_error() == 0
