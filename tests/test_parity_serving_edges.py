@@ -249,3 +249,83 @@ def test_every_error_since_the_last_check_is_named():
     assert isoq.isoq_check_device_error() == isoq.ISOQ_ERR_INVALID_ARG
     assert all(w in isoq.last_error() for w in said), isoq.last_error()
     assert isoq.isoq_check_device_error() == 0
+
+
+def _row_tile_ranks(b, tq, hq, hkv, tmax, window, n_sink):
+    """CTAs that share a row tile's tokens in the d = 128 windowed prefill."""
+    per = 128 // (hq // hkv)
+    ctas = -(-tq // per) * hkv * b
+    w, s = min(window + per, tmax), min(n_sink, tmax)
+    blocks, near, sink = -(-tmax // 32), -(-w // 32) + 1, -(-s // 32)
+    if near < blocks and sink < blocks and near + sink < blocks:
+        blocks = near + sink
+    return max(1, min(148 // ctas, 8, (blocks // 4 + 1) // 2))
+
+
+@pytest.mark.parametrize("b,tq,hq,hkv,lens,window,n_sink,ranks", [
+    (1, 8, 8, 1, [3971], 4000, 0, 8), (1, 16, 8, 1, [2500], 1500, 300, 7), (1, 100, 8, 4, [3000], 2000, 5, 8),
+    (3, 30, 4, 4, [3999, 700, 29], 4000, 0, 8), (2, 60, 8, 8, [1300, 1111], 900, 40, 5), (1, 1, 1, 1, [1700], 1500, 130, 7),
+    (1, 1, 2, 2, [700], 400, 100, 3), (2, 40, 8, 8, [4000, 260], 2600, 700, 8), (1, 130, 1, 1, [2047], 1, 2047, 8),
+    (1, 4, 8, 1, [5], 4000, 9, 8)])
+def test_prefill_clusters_of_every_size(b, tq, hq, hkv, lens, window, n_sink, ranks):
+    """Clusters of 3 to 8 CTAs, odd ones among them, whose shares of a row
+    tile's tokens are uneven or empty, sinks in other CTAs than the window."""
+    tmax = 4000
+    assert _row_tile_ranks(b, tq, hq, hkv, tmax, window, n_sink) == ranks
+    g = np.random.default_rng(ranks + tq)
+    cache, par = _cache(g, (b, hkv, tmax), 128, 3), _params(hkv, 128, 0)
+    q, lens = g.standard_normal((b, tq, hq, 128)).astype(F16), np.array(lens, np.int32)
+    got = isoq.isoq_prefill_attention_window(_t(q), *map(_t, cache), _t(lens), *map(_t, par), 3, 0, window, n_sink)
+    rows = sorted({0, tq // 3, tq // 2, tq - 1})
+    ref = S.window_prefill(q, *cache, lens, *par, 3, 0, 1 / np.sqrt(128), window, n_sink, rows=rows)
+    _check(got[:, rows], ref[:, rows], F16, q, cache[2], cache[3], 1 / np.sqrt(128))
+
+
+def _four_bytes_on(x):
+    """The same float16 tensor, its data 4 bytes past an 8-byte boundary."""
+    flat = torch.zeros(x.numel() + 8, dtype=x.dtype, device=x.device)
+    at = 2 if flat.data_ptr() % 8 == 0 else 0
+    flat = flat[at:at + x.numel()].view(x.shape)
+    assert flat.data_ptr() % 8 == 4
+    return flat.copy_(x)
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (8, 2), (16, 2)])
+@pytest.mark.parametrize("variant", [isoq.ISOQ_FULL, isoq.ISOQ_FAST])
+@pytest.mark.parametrize("which", ["q", "out"])
+def test_window_prefill_of_queries_off_an_8_byte_boundary(hq, hkv, variant, which):
+    """d = 128 with q or out aligned to 4 bytes only: the other kernel."""
+    g = np.random.default_rng(hq)
+    tmax, tq = 328, 70
+    lens = np.array([328, 90], np.int32)
+    cache, par = _cache(g, (2, hkv, tmax), 128, 3), _params(hkv, 128, variant)
+    q = g.standard_normal((2, tq, hq, 128)).astype(F16)
+    dq = _t(q)
+    out = torch.empty_like(dq)
+    if which == "q":
+        dq = _four_bytes_on(dq)
+    else:
+        out = _four_bytes_on(out)
+    for window, n_sink in [(100, 70), (9999, 0)]:
+        got = isoq.isoq_prefill_attention_window(dq, *map(_t, cache), _t(lens), *map(_t, par), 3, variant, window, n_sink, out=out)
+        assert got is out
+        ref = S.window_prefill(q, *cache, lens, *par, 3, variant, 1 / np.sqrt(128), window, n_sink)
+        _check(got, ref, F16, q, cache[2], cache[3], 1 / np.sqrt(128))
+
+
+@pytest.mark.parametrize("d,b,hq,hkv", [(128, 10, 4, 2), (128, 60, 3, 1), (256, 26, 2, 2), (256, 40, 8, 2)])
+@pytest.mark.parametrize("tmax", [41, 4097])
+def test_prefix_on_tcgen05_with_own_caches_of_odd_rooms(d, b, hq, hkv, tmax):
+    """The prefix on tcgen05, the rows' own caches (a room that is no multiple
+    of 8) on the CUDA cores."""
+    g = np.random.default_rng(b + tmax)
+    tp = 333
+    cache, prefix, par = _cache(g, (b, hkv, tmax), d, 3), _cache(g, (hkv, tp), d, 3), _params(hkv, d, 0)
+    q = g.standard_normal((b, hq, d)).astype(F16)
+    lens = g.integers(0, tmax + 1, b).astype(np.int32)
+    lens[:2] = 0, tmax
+    got = isoq.isoq_decode_attention_prefix(_t(q), *map(_t, prefix), _t(np.array([tp], np.int32)), *map(_t, cache), _t(lens),
+                                            *map(_t, par), 3, 0)
+    rows = [0, 1, 2, b // 2, b - 1]
+    ref = S.prefix_decode(q[rows], prefix, tp, *[c[rows] for c in cache], lens[rows], *par, 3, 0, 1 / np.sqrt(d))
+    _check(got[rows], ref, F16, q, cache[2], cache[3], 1 / np.sqrt(d))
