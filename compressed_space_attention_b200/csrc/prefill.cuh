@@ -303,13 +303,14 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   const int G = a.group;
 
   const int32_t *lens = PREFIX ? a.prefix_len : a.seq_lens + b;
-  int len = *lens;
-  len = len < 0 ? 0 : (len > a.tmax ? static_cast<int>(a.tmax) : len);
-  const int pos_base = PREFIX ? 0 : *lens - a.tq;
+  // Positions follow the length as given, also beyond the room; below 0 as 0.
+  // None of them, dead rows' among them, may leave the range of an int.
+  const int given = *lens < 0 ? 0 : *lens;
+  const int len = given > a.tmax ? static_cast<int>(a.tmax) : given;
+  const int pos_base = PREFIX ? 0 : given - a.tq;
   const int tq0 = PREFIX ? 0 : qt * BQ;
   const int p_first = PREFIX ? 0x7FFFFF00 : pos_base + tq0;   // (every token is at or before it)
-  int p_last = pos_base + tq0 + BQ - 1;
-  if (tq0 + BQ > a.tq) p_last = pos_base + a.tq - 1;
+  const int p_last = pos_base + (tq0 + BQ > a.tq ? a.tq : tq0 + BQ) - 1;
   int tend = p_last + 1 < len ? p_last + 1 : len;
   if (tend < 0) tend = 0;
   int n_tiles = (tend + kTcTok - 1) / kTcTok;
@@ -478,9 +479,8 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   };
 
   const int r = 32 * sub + lane;                              // this thread's row / TMEM lane
-  const int pr = p_first + r / GP;
-  const int pw_min = p_first + (32 * sub) / GP;
-  const int pw_max = p_first + (32 * sub + 31) / GP;
+  auto position = [&](int row) { return PREFIX ? p_first + row / GP : p_first + min(row / GP, p_last - p_first); };
+  const int pr = position(r), pw_min = position(32 * sub), pw_max = position(32 * sub + 31);
   constexpr int HC = kTcTok / 2;                               // score columns per thread
   constexpr int OH = D / 2;                                    // output columns per thread
   float mx = -INFINITY;

@@ -125,16 +125,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
 
   // ---- the CTA's rows and tokens ----
   const int32_t *lens = WIN ? a.seq_lens + b : a.prefix_len;
-  int len = *lens;
-  len = len < 0 ? 0 : (len > a.tmax ? static_cast<int>(a.tmax) : len);
+  // (Positions follow the length as given, also beyond the room; below 0 as 0.)
+  const int given = *lens < 0 ? 0 : *lens;
+  const int len = given > a.tmax ? static_cast<int>(a.tmax) : given;
   const int per_cta = kTcRows / (WIN ? G : 1);               // kPfWindow: positions of the CTA
   const int tq0 = WIN ? qt * per_cta : 0;
-  const int p_first = WIN ? *lens - a.tq + tq0 : 0;          // position of the CTA's first row
+  const int p_first = WIN ? given - a.tq + tq0 : 0;          // position of the CTA's first row
   const int total_rows = WIN ? 0 : a.batch * G;
   int tend, t_base = 0, n_sink_tiles = 0, win_tile = 0, sink = 0, lo = 0, n_iter, j_base = 0;
   if constexpr (WIN) {
-    int p_last = p_first + per_cta - 1;
-    if (tq0 + per_cta > a.tq) p_last = *lens - 1;
+    const int p_last = tq0 + per_cta > a.tq ? given - 1 : p_first + per_cta - 1;
     tend = p_last + 1 < len ? p_last + 1 : len;
     if (tend < 0) tend = 0;
     const int all = (tend + kRowsTok - 1) / kRowsTok;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
     // The last token the row sees, and the last one behind its window.
     int p_row = 0x7FFFFFFF, behind = -1, n_sink = 0;
     if constexpr (WIN) {
-      p_row = p_first + i / G;
+      p_row = p_first + min(i / G, a.tq - 1 - tq0);   // (a dead row: the last one's)
       behind = p_row >= a.window ? p_row - a.window : -1;
       n_sink = a.n_sink;
     }

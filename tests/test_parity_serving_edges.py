@@ -329,3 +329,20 @@ def test_prefix_on_tcgen05_with_own_caches_of_odd_rooms(d, b, hq, hkv, tmax):
     rows = [0, 1, 2, b // 2, b - 1]
     ref = S.prefix_decode(q[rows], prefix, tp, *[c[rows] for c in cache], lens[rows], *par, 3, 0, 1 / np.sqrt(d))
     _check(got[rows], ref, F16, q, cache[2], cache[3], 1 / np.sqrt(d))
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 2, 2), (128, 8, 1), (256, 2, 2), (256, 8, 1)])
+def test_prefill_at_positions_next_to_the_largest(d, hq, hkv):
+    """Lengths at both ends of int32 (the cache holds the first Tmax tokens of
+    so long a row): the positions of a tile's rows do not wrap around."""
+    g = np.random.default_rng(d + hq)
+    tmax, tq, top = 320, 24, 2 ** 31 - 1
+    lens = np.array([top, top - 60, -2 ** 31, 300], np.int32)
+    cache, par = _cache(g, (4, hkv, tmax), d, 3), _params(hkv, d, 0)
+    q = g.standard_normal((4, tq, hq, d)).astype(F16)
+    for window, n_sink in [(top - 150, 0), (top - 100, 33), (top, 0), (64, 10)]:
+        got = isoq.isoq_prefill_attention_window(_t(q), *map(_t, cache), _t(lens), *map(_t, par), 3, 0, window, n_sink)
+        rows = [0, 11, 23]
+        ref = S.window_prefill(q, *cache, lens, *par, 3, 0, 1 / np.sqrt(d), window, n_sink, rows=rows)
+        _check(got[:, rows], ref[:, rows], F16, q, cache[2], cache[3], 1 / np.sqrt(d))
+        assert not got[2].any()
