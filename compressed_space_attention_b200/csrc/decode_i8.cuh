@@ -1,6 +1,6 @@
 // Integer tensor-core split kernel of the compressed-space decode: float16
 // queries, 3-bit codes, d in {128, 256}, up to 8 query heads per KV head.
-// Included by isoq_decode.cu inside namespace isoq::decode.
+// Included by isoq_decode.cu and isoq_serve.cu inside namespace isoq::decode.
 //
 // The work per token is RotaryQuant Table 2 kernels A-C on the packed codes:
 // z_j = s^K_j <q~, c[K_j]> scale, online softmax, acc += p_j s^V_j c[V_j], all
