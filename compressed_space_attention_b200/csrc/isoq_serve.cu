@@ -141,10 +141,11 @@ inline int resident_ctas(bool i8, int d, int bits, int rows) {
 
 // Small problems run as one launch: up to 8 splits of a row group form a
 // cluster that merges its partial states itself.  Taken where 8 splits of at
-// most 16 blocks cover the longest list and all CTAs are resident at once.  1 row, 32 query over 4 KV heads, 1,028 tokens: 12.3 us on the GPU
-// against 10.3 for the three launches, but 5.3 us of host time to queue it
-// against 9.9 (and no workspace): with the Python call around it a step of many
-// layers is bound by the queueing, 13.4 us a call against 19.2.
+// most 16 blocks cover the longest list and all CTAs are resident at once.
+// 1 row, 32 query over 4 KV heads, 1,028 tokens: 12.3 us on the GPU against 10.3
+// for the three launches, but 5.3 us of host time to queue it against 9.9 (and
+// no workspace): with the Python call around it a step of many layers is bound
+// by the queueing, 13.4 us a call against 19.2.
 constexpr int kFusedSplits = kMaxClusterSplits, kFusedBlocks = 16;
 
 // The rows of a KV head's batch x group from which on the prefix goes to the

@@ -14,9 +14,10 @@
 // (8 bytes a request, from L2), and then writes its own share of the slots,
 // finding a token's request by bisection, and of the table rows.  One launch,
 // nothing exchanged between CTAs; at these sizes its cost is the launch and
-// two or three dependent reads (64 requests of one token 7 us with the copy of
-// the table before it, 512 requests and 43,000 slots 8 us; 14 us with 2,048
-// slots per CTA, whose reads follow one another).
+// two or three dependent reads (on the GPU 64 requests of one token take 7 us
+// with the copy of the table before it, 512 requests and 43,000 slots 8; 14
+// with 2,048 slots per CTA, whose reads follow one another; a call of either
+// with its host work 19).
 
 constexpr int kTableThreads = 256;
 constexpr int kTableRows = 1024;     // requests per pass

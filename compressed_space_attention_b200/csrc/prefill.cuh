@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(kTcThreads, TcCfg<D>::MIN_BLOCKS) prefill_tc_k
   int n_sink_tiles = 0, win_tile = 0, sink = 0, lo = 0;
   if constexpr (WIN) {
     sink = a.n_sink < tend ? a.n_sink : tend;
-    lo = p_first >= a.window ? p_first - a.window + 1 : 0;   // the first row's window begins here
+    // The first row's window begins at lo; a window of none holds no token.
+    lo = a.window == 0 ? tend : (p_first >= a.window ? p_first - a.window + 1 : 0);
     if (lo > tend) lo = tend;
     if (lo > sink) {
       const int all = n_tiles;

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
     if (tend < 0) tend = 0;
     const int all = (tend + kRowsTok - 1) / kRowsTok;
     sink = a.n_sink < tend ? a.n_sink : tend;
-    lo = p_first >= a.window ? p_first - a.window + 1 : 0;
+    lo = a.window == 0 ? tend : (p_first >= a.window ? p_first - a.window + 1 : 0);   // (no window holds no token)
     if (lo > tend) lo = tend;
     n_iter = all;
     if (lo > sink) {

@@ -19,9 +19,9 @@
 //   add the four slices and leave lane L with token L.
 //   Values: a lane takes d / 32 dimensions, the weights broadcast.
 //
-// Bound: issue slots and the ALU pipe (0.57 per cycle and 46 % busy): about 110
-// warp instructions per token and KV head for 8 rows, of which the two products
-// are 32, the code lookups 32.  16 rows of 4,096 to 8,192 tokens x 4 KV heads,
+// Bound: issue slots (0.59 per cycle), the ALU and FMA pipes (43 % busy each)
+// and the LSU pipe (36 %): about 110 warp instructions per token and KV head for
+// 8 rows, of which the two products are 32, the code lookups 32.  16 rows of 4,096 to 8,192 tokens x 4 KV heads,
 // d = 128, 4 bits, 8 rows: a token per lane in the score loop took 92 us (every
 // query value loaded again for each token), this form 78; half a warp per token
 // in the value loop 84 (168 registers, 3 CTAs per SM instead of 4).

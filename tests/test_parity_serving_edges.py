@@ -346,3 +346,28 @@ def test_prefill_at_positions_next_to_the_largest(d, hq, hkv):
         ref = S.window_prefill(q, *cache, lens, *par, 3, 0, 1 / np.sqrt(d), window, n_sink, rows=rows)
         _check(got[:, rows], ref[:, rows], F16, q, cache[2], cache[3], 1 / np.sqrt(d))
         assert not got[2].any()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("window", [0, 1])
+def test_small_v_norms_of_sinks_behind_an_empty_window(d, window):
+    """One sink of norm 0.002 (and, with a window of 1, the query's own token,
+    whose score is far lower): the output is the sink's V vector, whatever the
+    norms of the chunk's other tokens.  Tolerance as above."""
+    g = np.random.default_rng(d)
+    tmax, t, tq = 848, 468, 4
+    cache, par = _cache(g, (1, 1, tmax), d, 3), _params(1, d, 0)
+    cache[2][:], cache[3][:] = 1e-3, 65504
+    cache[2][..., 0], cache[3][..., 0] = 16, 0.002
+    own = list(range(t - tq, t))
+    cache[3][..., own if window else []] = 0.002
+    unit_k, unit_v = (O.dequantize(x[0, :, :1], np.ones((1, 1), F16), p, 3, 0, d)[0, 0] for x, p in zip(cache[:2], par))
+    q1 = g.standard_normal(d).astype(F16)
+    scale = 60 * np.log(2) / (16 * float(q1.astype(np.float64) @ unit_k))
+    q = np.tile(q1, (1, tq, 1, 1))
+    got = isoq.isoq_prefill_attention_window(_t(q), *map(_t, cache), _t(np.array([t], np.int32)), *map(_t, par), 3, 0, window, 1,
+                                             scale=scale)
+    assert isoq.isoq_check_device_error() == 0
+    ref = float(F16(0.002)) * unit_v
+    err = np.abs(got.cpu().numpy().astype(np.float64).reshape(-1, d) - ref)
+    assert (err <= f16_half_ulp(ref) + 2.0 ** -15 * float(F16(0.002))).all(), (err.max(), np.abs(ref).max())
