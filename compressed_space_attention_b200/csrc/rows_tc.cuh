@@ -33,11 +33,12 @@
 // buffers of K (hi, lo) and V, 192 KB, and four of the norms.
 //
 // Bound: the tensor core, five products of 128 x 128 x 128 per 128 tokens (2.5
-// times the operator's arithmetic), 56 % busy: about 4,200 cycles per 128 rows
+// times the operator's arithmetic), 57 % busy: about 4,200 cycles per 128 rows
 // and tokens, of which the score products take 2,200 and the value products
 // 1,350 (1,536 and 1,024 at the tensor core's rate), the softmax of a tile 3,300
-// beside them.  64 batch rows x 8 heads behind 65,536 tokens, 4 KV heads: 174 us;
-// 2 x 2,048 queries, 32 over 4 heads, window 2,048: 347 us.
+// beside them.  64 batch rows x 8 heads behind 65,536 tokens, 4 KV heads: 170 us
+// on the GPU, 184 a call with the own caches' split and the host's work; 2 x
+// 2,048 queries, 32 over 4 heads, window 2,048: 350 us.
 //
 // kPfWindow: rows are positions x heads of a chunk; rotation of the queries
 // before and of the output after the loop, both in the CTA.  Where the chunk
