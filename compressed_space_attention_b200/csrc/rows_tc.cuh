@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
     };
     auto largest = [](const Quat &y) { return fmaxf(fmaxf(fabsf(y.w), fabsf(y.x)), fmaxf(fabsf(y.y), fabsf(y.z))); };
     // Bit k: row k of the warp has a component of 1/4 or more (or no query),
-    // bit 8 + k: one of 2^15 or more.  Rows that need a scale are done again
-    // (a maximum over the warp in every row's chain cost 1.3 us of a CTA).
+    // bit 8 + k: one of 2^15 or more.  Rows that need a scale are done again, so
+    // that no maximum over the warp stands in every row's chain.
     uint32_t range = 0;
     for (int i = warp, k = 0; i < kTcRows; i += kRowsWarps, ++k) {
       const long long row = query_of(i);
@@ -335,119 +335,120 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_tc_kernel(const PrefillA
     float ref = -INFINITY;
     uint64_t la = f2_pack(0.f, 0.f), lb = la;
     auto tiles = [&](auto scaled) {
-    constexpr bool SCALED = decltype(scaled)::value;
-    for (int j = 0; j < n_iter; ++j) {
-      // (After a wait that gave up the loop goes on without waiting, so that
-      // the barriers of a pair of warps always meet.)
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(s_full + (j & 1), (j >> 1) & 1) &&
-                                               mbar_wait_bounded(n_full + (j & 3), (j >> 2) & 1));
-      tc_fence_after();
-      const uint32_t t_s = tmem + 128 * (j & 1) + 64 * half + lane_off;
-      const int t0 = tile_t0(j) + 64 * half;
-      const float *nk = norms + (j & 3) * 2 * kRowsTok + 64 * half, *nv = nk + kRowsTok;
-      // Which columns the row sees, 32 at a time.
-      uint32_t vis[2];
+      constexpr bool SCALED = decltype(scaled)::value;
+      for (int j = 0; j < n_iter; ++j) {
+        // (After a wait that gave up the loop goes on without waiting, so that
+        // the barriers of a pair of warps always meet.)
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(s_full + (j & 1), (j >> 1) & 1) &&
+                                                 mbar_wait_bounded(n_full + (j & 3), (j >> 2) & 1));
+        tc_fence_after();
+        const uint32_t t_s = tmem + 128 * (j & 1) + 64 * half + lane_off;
+        const int t0 = tile_t0(j) + 64 * half;
+        const float *nk = norms + (j & 3) * 2 * kRowsTok + 64 * half, *nv = nk + kRowsTok;
+        // Which columns the row sees, 32 at a time.
+        uint32_t vis[2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int cb = t0 + 32 * c;
-        vis[c] = bits_below(last - cb + 1);
-        if constexpr (WIN) vis[c] &= bits_below(n_sink - cb) | ~bits_below(behind - cb + 1);
-      }
-      const bool part = __any_sync(0xffffffffu, (vis[0] & vis[1]) != 0xFFFFFFFFu);
-      uint32_t s[2][32];
-      tc_ld32(t_s, s[0]);
-      tc_ld32(t_s + 32, s[1]);
-      tc_ld32_done(s[0]);
-      tc_ld32_done(s[1]);
-      // x = S s^K scale (log2 domain), in place, and the row's maximum
-      float x[2][32], m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const ulonglong2 *n4 = reinterpret_cast<const ulonglong2 *>(nk + 32 * c);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const ulonglong2 n = n4[k];
-          f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c][4 * k]), __uint_as_float(s[c][4 * k + 1])), n.x), x[c][4 * k], x[c][4 * k + 1]);
-          f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c][4 * k + 2]), __uint_as_float(s[c][4 * k + 3])), n.y), x[c][4 * k + 2], x[c][4 * k + 3]);
+        for (int c = 0; c < 2; ++c) {
+          const int cb = t0 + 32 * c;
+          vis[c] = bits_below(last - cb + 1);
+          if constexpr (WIN) vis[c] &= bits_below(n_sink - cb) | ~bits_below(behind - cb + 1);
         }
-        if constexpr (SCALED) {
+        const bool part = __any_sync(0xffffffffu, (vis[0] & vis[1]) != 0xFFFFFFFFu);
+        uint32_t s[2][32];
+        tc_ld32(t_s, s[0]);
+        tc_ld32(t_s + 32, s[1]);
+        tc_ld32_done(s[0]);
+        tc_ld32_done(s[1]);
+        // x = S s^K scale (log2 domain), in place, and the row's maximum
+        float x[2][32], m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[c][e] *= back;
+        for (int c = 0; c < 2; ++c) {
+          const ulonglong2 *n4 = reinterpret_cast<const ulonglong2 *>(nk + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const ulonglong2 n = n4[k];
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c][4 * k]), __uint_as_float(s[c][4 * k + 1])), n.x), x[c][4 * k], x[c][4 * k + 1]);
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c][4 * k + 2]), __uint_as_float(s[c][4 * k + 3])), n.y), x[c][4 * k + 2], x[c][4 * k + 3]);
+          }
+          if constexpr (SCALED) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c][e] *= back;
+          }
+          if (part) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c][e] = (vis[c] >> e) & 1u ? x[c][e] : -INFINITY;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[c][e]);
         }
-        if (part) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[c][e] = (vis[c] >> e) & 1u ? x[c][e] : -INFINITY;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], x[c][e]);
-      }
-      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      float *xm = xchg + (j & 1) * 2 * kTcRows;
-      xm[half * kTcRows + i] = mx;
-      named_barrier(1 + (warp & 3), 64);
-      mx = fmaxf(mx, xm[(half ^ 1) * kTcRows + i]);
-      // Move the reference (both warps of the pair alike); O follows, once its
-      // last product is complete.
-      if (__any_sync(0xffffffffu, mx > ref)) {
-        const bool move = mx > ref;
-        const float nref = move ? mx + kRowsHeadroom : ref;
-        const float f = move ? ex2f(ref - nref) : 1.f;      // 0 while ref = -inf
-        ref = nref;
-        const uint64_t f2 = f2_pack(f, f);
-        la = f2_mul(la, f2);
-        lb = f2_mul(lb, f2);
-        if (j > 0) {
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_done, (j - 1) & 1));
-          tc_fence_after();
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        float *xm = xchg + (j & 1) * 2 * kTcRows;
+        xm[half * kTcRows + i] = mx;
+        named_barrier(1 + (warp & 3), 64);
+        mx = fmaxf(mx, xm[(half ^ 1) * kTcRows + i]);
+        // Move the reference (both warps of the pair alike); O follows, once its
+        // last product is complete.
+        if (__any_sync(0xffffffffu, mx > ref)) {
+          const bool move = mx > ref;
+          const float nref = move ? mx + kRowsHeadroom : ref;
+          const float f = move ? ex2f(ref - nref) : 1.f;      // 0 while ref = -inf
+          ref = nref;
+          const uint64_t f2 = f2_pack(f, f);
+          la = f2_mul(la, f2);
+          lb = f2_mul(lb, f2);
+          if (j > 0) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_done, (j - 1) & 1));
+            tc_fence_after();
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            float v[16];
-            tc_ld16(t_o + 64 * half + lane_off + 16 * k, v);
+            for (int k = 0; k < 4; ++k) {
+              float v[16];
+              tc_ld16(t_o + 64 * half + lane_off + 16 * k, v);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) f2_unpack(f2_mul(f2_pack(v[e], v[e + 1]), f2), v[e], v[e + 1]);
-            tc_st16(t_o + 64 * half + lane_off + 16 * k, v);
-          }
-        }
-      }
-      const float base = ref == -INFINITY ? 0.f : ref;
-      const uint64_t base2 = f2_pack(base, base);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {   // 16 scores: 8 columns of hi and 8 of lo parts
-        const ulonglong2 *v4 = reinterpret_cast<const ulonglong2 *>(nv + 16 * c);
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const ulonglong2 w = v4[k];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int q = 16 * (c & 1) + 4 * k + 2 * e;
-            float x0, x1, w0, w1, d0, d1;
-            f2_unpack(f2_sub(f2_pack(x[c >> 1][q], x[c >> 1][q + 1]), base2), x0, x1);
-            const uint64_t p2 = f2_pack(ex2f(x0), ex2f(x1));
-            if (e) lb = f2_add(lb, p2); else la = f2_add(la, p2);
-            f2_unpack(f2_mul(p2, e ? w.y : w.x), w0, w1);
-            if (part) {   // a token that is not seen weighs nothing, whatever its norm holds
-              w0 = (vis[c >> 1] >> q) & 1u ? w0 : 0.f;
-              w1 = (vis[c >> 1] >> (q + 1)) & 1u ? w1 : 0.f;
+              for (int e = 0; e < 16; e += 2) f2_unpack(f2_mul(f2_pack(v[e], v[e + 1]), f2), v[e], v[e + 1]);
+              tc_st16(t_o + 64 * half + lane_off + 16 * k, v);
             }
-            const __half2 h = __floats2half2_rn(w0, w1);
-            const float2 hf = __half22float2(h);
-            hi[2 * k + e] = *reinterpret_cast<const uint32_t *>(&h);
-            f2_unpack(f2_sub(f2_pack(w0, w1), f2_pack(hf.x, hf.y)), d0, d1);
-            lo[2 * k + e] = pack_f16x2(d0, d1);
           }
         }
-        tc_st8u(t_s + 32 * (c >> 1) + 8 * (c & 1), hi);
-        tc_st8u(t_s + 32 * (c >> 1) + 16 + 8 * (c & 1), lo);
+        const float base = ref == -INFINITY ? 0.f : ref;
+        const uint64_t base2 = f2_pack(base, base);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {   // 16 scores: 8 columns of hi and 8 of lo parts
+          const ulonglong2 *v4 = reinterpret_cast<const ulonglong2 *>(nv + 16 * c);
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const ulonglong2 w = v4[k];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int q = 16 * (c & 1) + 4 * k + 2 * e;
+              float x0, x1, w0, w1, d0, d1;
+              f2_unpack(f2_sub(f2_pack(x[c >> 1][q], x[c >> 1][q + 1]), base2), x0, x1);
+              const uint64_t p2 = f2_pack(ex2f(x0), ex2f(x1));
+              if (e) lb = f2_add(lb, p2); else la = f2_add(la, p2);
+              f2_unpack(f2_mul(p2, e ? w.y : w.x), w0, w1);
+              if (part) {   // a token that is not seen weighs nothing, whatever its norm holds
+                w0 = (vis[c >> 1] >> q) & 1u ? w0 : 0.f;
+                w1 = (vis[c >> 1] >> (q + 1)) & 1u ? w1 : 0.f;
+              }
+              const __half2 h = __floats2half2_rn(w0, w1);
+              const float2 hf = __half22float2(h);
+              hi[2 * k + e] = *reinterpret_cast<const uint32_t *>(&h);
+              f2_unpack(f2_sub(f2_pack(w0, w1), f2_pack(hf.x, hf.y)), d0, d1);
+              lo[2 * k + e] = pack_f16x2(d0, d1);
+            }
+          }
+          tc_st8u(t_s + 32 * (c >> 1) + 8 * (c & 1), hi);
+          tc_st8u(t_s + 32 * (c >> 1) + 16 + 8 * (c & 1), lo);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + (j & 1));
       }
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + (j & 1));
-    }
     };
     // Two versions of the loop: the factor (or a branch around it) in the one
-    // that hardly a call needs it in costs 1.3 % of the windowed prefill.
+    // that hardly a call needs it in costs 1.2 % of the windowed prefill (355
+    // against 351 us).
     if (__any_sync(0xffffffffu, back != 1.f))
       tiles(std::true_type{});
     else

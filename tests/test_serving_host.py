@@ -196,13 +196,3 @@ def test_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(ValueError, match="fewer entries"):
         isoq.isoq_paged_append(f16(3, 2, 128), f16(3, 2, 128), u8(4, 2, 16, 48), u8(4, 2, 16, 48), f16(4, 2, 16),
                                f16(4, 2, 16), torch.zeros(2, dtype=torch.int64), pr, pr, 3, 0)
-
-
-def test_one_launch_only_where_its_clusters_are_resident():
-    """A cluster launch needs no workspace and is taken where the SMs hold all
-    its CTAs at once: 148 x 1 at d = 512 with 3 or 4 bits, where 32 rows x 4 KV
-    heads leave room for one split of a row's 1,024 tokens and two are needed."""
-    w = isoq.isoq_decode_window_workspace_size
-    assert w(32, 4, 4, 1024, 512, 1024, 0) > 0
-    assert w(16, 4, 4, 1024, 512, 1024, 0) == 0      # 64 clusters of two
-    assert w(32, 4, 4, 1024, 128, 1024, 0) == 0      # 4 per SM
